@@ -43,6 +43,14 @@ __all__ = [
     "UpdateConfig",
     "cconv_default_update_config",
     "cconv_default_config",
+    "cconv_linattn_fwd",
+    "cconv_linattn_bwd",
+    "cconv_linattn_update",
+    "cconv_linattn_fwd_workspace_bytes",
+    "cconv_linattn_bwd_workspace_bytes",
+    "cconv_qknorm_fwd",
+    "cconv_qknorm_bwd",
+    "cconv_qknorm_bwd_workspace_bytes",
     "cconv_status_string",
     "cconv_version",
     "STATUS",
@@ -162,6 +170,12 @@ class BwdOpts(ctypes.Structure):
     ]
 
 
+class Rows(ctypes.Structure):
+    """cconv_rows_t."""
+
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_int64), ("st", ctypes.c_int64), ("sh", ctypes.c_int64)]
+
+
 ACTIVATIONS = {"silu": 1, "swish": 1, None: 0, "none": 0}
 
 
@@ -221,6 +235,23 @@ def _declare(L):
     L.cconv_default_update_config.restype = i32
     L.cconv_default_config.argtypes = [i32, i64, i64, i64, i32, ctypes.POINTER(Config)]
     L.cconv_default_config.restype = i32
+    r, f = ctypes.POINTER(Rows), ctypes.c_float
+    L.cconv_linattn_fwd_workspace_bytes.argtypes = [i64] * 6
+    L.cconv_linattn_fwd_workspace_bytes.restype = sz
+    L.cconv_linattn_fwd.argtypes = [r, r, r, p, f, p, r, p, p, i64, p, p, sz, i64, i64, i64, i64, i64, i64, p]
+    L.cconv_linattn_fwd.restype = i32
+    L.cconv_linattn_bwd_workspace_bytes.argtypes = [i64] * 7
+    L.cconv_linattn_bwd_workspace_bytes.restype = sz
+    L.cconv_linattn_bwd.argtypes = [r, r, r, p, f, p, r, p, r, r, r, p, p, i64, p, p, sz] + [i64] * 6 + [p]
+    L.cconv_linattn_bwd.restype = i32
+    L.cconv_linattn_update.argtypes = [r, r, r, p, f, p, i64, p, r, i64, i64, i64, i64, i64, p, p]
+    L.cconv_linattn_update.restype = i32
+    L.cconv_qknorm_fwd.argtypes = [r, r, p, p, i32, p, i64, i64, i32, p, f, r, r] + [i64] * 5 + [p, p]
+    L.cconv_qknorm_fwd.restype = i32
+    L.cconv_qknorm_bwd_workspace_bytes.argtypes = [i64] * 5
+    L.cconv_qknorm_bwd_workspace_bytes.restype = sz
+    L.cconv_qknorm_bwd.argtypes = [r, r, r, r, p, p, i32, p, i64, i64, i32, p, f, r, r, p, p, p, sz] + [i64] * 5 + [p, p]
+    L.cconv_qknorm_bwd.restype = i32
     L.cconv_status_string.argtypes = [i32]
     L.cconv_status_string.restype = ctypes.c_char_p
     L.cconv_version.argtypes = []
@@ -1020,3 +1051,267 @@ def cconv_bwd_ex(x, dy, w, bias=None, *, activation="silu", init_state=None, d_i
                               _ptr(dw), _wdt(dw, "dw"), _ptr(dbias), _ptr(workspace), ws_bytes, B, T, D, W,
                               ctypes.byref(o), _stream(stream)), "cconv_bwd_ex")
     return dx, dw, dbias, d_init_state, status
+
+
+# ---- linear attention with a decay for each head, and the norm of query and key heads -------
+
+
+def _heads(t, name: str, shape=None, packed: bool = False) -> Rows:
+    """bf16 rows of heads, [B, T, H, D] (packed batches and single tokens: [rows, H, D]) with unit
+    channel stride, as the library takes them; `shape`: what it must have."""
+    _dev(t, name)
+    d = 3 if packed else 4
+    if t.dtype != torch.bfloat16 or t.dim() != d or (t.stride(d - 1) != 1 and t.shape[d - 1] > 1):
+        kind = "[rows, H, D]" if packed else "[B, T, H, D]"
+        raise ValueError(f"{name} must be bf16 {kind} with unit channel stride")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
+    st = t.stride()
+    return Rows(t.data_ptr(), 0, st[0], st[1]) if packed else Rows(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _decay(log_decay, HV: int):
+    _dev(log_decay, "log_decay")
+    if log_decay.dtype != torch.float32 or log_decay.shape != (HV,) or not log_decay.is_contiguous():
+        raise ValueError("log_decay must be a contiguous fp32 [HV] tensor")
+
+
+def _workspace(t, need: int, dev):
+    """The caller's workspace, or a new one; (tensor or None, bytes)."""
+    if t is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+    return t, _ws(t)
+
+
+def cconv_linattn_fwd_workspace_bytes(B, T, HV, Dk, Dv, nseq: int = -1) -> int:
+    return int(lib().cconv_linattn_fwd_workspace_bytes(B, T, nseq, HV, Dk, Dv))
+
+
+def cconv_linattn_bwd_workspace_bytes(B, T, H, HV, Dk, Dv, nseq: int = -1) -> int:
+    return int(lib().cconv_linattn_bwd_workspace_bytes(B, T, nseq, H, HV, Dk, Dv))
+
+
+def _linattn_sizes(q, v, cu_seqlens):
+    """(B, T, H, HV, Dk, Dv, state rows, nseq or -1) of q [B, T, H, Dk] and v [B, T, HV, Dv] (packed:
+    [total, ., .] with cu_seqlens)."""
+    packed = cu_seqlens is not None
+    d = 3 if packed else 4
+    if q.dim() != d or v.dim() != d:
+        raise ValueError("q and v must be [total, H, D] with cu_seqlens, [B, T, H, D] without")
+    H, Dk = q.shape[-2:]
+    HV, Dv = v.shape[-2:]
+    if packed:
+        _dev(cu_seqlens, "cu_seqlens")
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 \
+                or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be a contiguous int32 [nseq + 1] tensor")
+        n = cu_seqlens.numel() - 1
+        return 1, q.shape[0], H, HV, Dk, Dv, n, n
+    return q.shape[0], q.shape[1], H, HV, Dk, Dv, q.shape[0], -1
+
+
+def cconv_linattn_fwd(q, k, v, log_decay, *, scale: float = 1.0, init_state=None, final_state=None,
+                      want_final_state: bool = False, cu_seqlens=None, o=None, status=None, workspace=None, stream=None):
+    """Linear attention with a decay for each value head: S_t = exp(log_decay) S_{t-1} + k_t^T v_t,
+    o_t = scale * q_t S_t. Returns (o, final_state, status).
+
+    q, k: bf16 [B, T, H, Dk]; v: bf16 [B, T, HV, Dv], HV a multiple of H (any strides with contiguous
+    channels); log_decay: fp32 [HV]; states: fp32 [B, HV, Dk, Dv]. With cu_seqlens (int32 [nseq+1])
+    the tensors are packed [total, ., .] and the states [nseq, ...]; status (a device int32, None for
+    fixed lengths) then receives 0, or 8 for offsets that do not partition the rows.
+    """
+    packed = cu_seqlens is not None
+    B, T, H, HV, Dk, Dv, n, nseq = _linattn_sizes(q, v, cu_seqlens)
+    rq, rk, rv = _heads(q, "q", None, packed), _heads(k, "k", q.shape, packed), _heads(v, "v", q.shape[:-2] + v.shape[-2:], packed)
+    _decay(log_decay, HV)
+    dev = q.device
+    _out(init_state, "init_state", (n, HV, Dk, Dv), _F32)
+    if final_state is None:
+        if want_final_state:
+            final_state = torch.empty((n, HV, Dk, Dv), dtype=torch.float32, device=dev)
+    else:
+        _out(final_state, "final_state", (n, HV, Dk, Dv), _F32)
+    if o is None:
+        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    ro = _heads(o, "o", v.shape, packed)
+    if packed:
+        if status is None:
+            status = torch.empty(1, dtype=torch.int32, device=dev)
+        _out(status, "status", (1,), _I32)
+    else:
+        status = None
+    L = lib()
+    workspace, ws_bytes = _workspace(workspace, L.cconv_linattn_fwd_workspace_bytes(B, T, nseq, HV, Dk, Dv), dev)
+    _check(L.cconv_linattn_fwd(rq, rk, rv, _ptr(log_decay), scale, _ptr(init_state), ro, _ptr(final_state),
+                               _ptr(cu_seqlens), nseq, _ptr(status), _ptr(workspace), ws_bytes, B, T, H, HV, Dk, Dv,
+                               _stream(stream)), "cconv_linattn_fwd")
+    return o, final_state, status
+
+
+def cconv_linattn_bwd(q, k, v, log_decay, d_o, *, scale: float = 1.0, init_state=None, d_final_state=None,
+                      want_d_init_state: bool = False, d_init_state=None, cu_seqlens=None, dq=None, dk=None, dv=None,
+                      status=None, workspace=None, stream=None):
+    """Gradients of cconv_linattn_fwd for the gradients d_o of o and d_final_state (or None) of the
+    final state. Returns (dq, dk, dv, d_init_state or None, status). dq and dk are summed over a
+    group's value heads in fp32."""
+    packed = cu_seqlens is not None
+    B, T, H, HV, Dk, Dv, n, nseq = _linattn_sizes(q, v, cu_seqlens)
+    rq, rk, rv = _heads(q, "q", None, packed), _heads(k, "k", q.shape, packed), _heads(v, "v", q.shape[:-2] + v.shape[-2:], packed)
+    rdo = _heads(d_o, "d_o", v.shape, packed)
+    _decay(log_decay, HV)
+    dev = q.device
+    _out(init_state, "init_state", (n, HV, Dk, Dv), _F32)
+    _out(d_final_state, "d_final_state", (n, HV, Dk, Dv), _F32)
+    if d_init_state is None:
+        if want_d_init_state:
+            d_init_state = torch.empty((n, HV, Dk, Dv), dtype=torch.float32, device=dev)
+    else:
+        _out(d_init_state, "d_init_state", (n, HV, Dk, Dv), _F32)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if dk is None:
+        dk = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    outs = _heads(dq, "dq", q.shape, packed), _heads(dk, "dk", q.shape, packed), _heads(dv, "dv", v.shape, packed)
+    if packed:
+        if status is None:
+            status = torch.empty(1, dtype=torch.int32, device=dev)
+        _out(status, "status", (1,), _I32)
+    else:
+        status = None
+    L = lib()
+    workspace, ws_bytes = _workspace(workspace, L.cconv_linattn_bwd_workspace_bytes(B, T, nseq, H, HV, Dk, Dv), dev)
+    _check(L.cconv_linattn_bwd(rq, rk, rv, _ptr(log_decay), scale, _ptr(init_state), rdo, _ptr(d_final_state), *outs,
+                               _ptr(d_init_state), _ptr(cu_seqlens), nseq, _ptr(status), _ptr(workspace), ws_bytes, B, T,
+                               H, HV, Dk, Dv, _stream(stream)), "cconv_linattn_bwd")
+    return dq, dk, dv, d_init_state, status
+
+
+def cconv_linattn_update(q, k, v, log_decay, state, state_indices=None, *, scale: float = 1.0, o=None, status=None,
+                         stream=None):
+    """One token of N sequences on a pool of states (fp32 [S, HV, Dk, Dv], updated in place): row n's
+    slot is state_indices[n] (int32 [N]; -1: padding, o = 0) or n. q, k: bf16 [N, H, Dk]; v: bf16
+    [N, HV, Dv]. Returns (o, status); status (device int32) receives 0, or 8 for bad or repeated
+    slots, in which case no state was written."""
+    rq, rk = _heads(q, "q", None, True), _heads(k, "k", q.shape, True)
+    N, H, Dk = q.shape
+    rv = _heads(v, "v", None, True)
+    if v.shape[0] != N:
+        raise ValueError("v must have q's rows")
+    HV, Dv = v.shape[1:]
+    _decay(log_decay, HV)
+    _dev(state, "state")
+    if state.dtype != torch.float32 or state.dim() != 4 or state.shape[1:] != (HV, Dk, Dv) or not state.is_contiguous():
+        raise ValueError("state must be a contiguous fp32 [S, HV, Dk, Dv] tensor")
+    idx = None
+    if state_indices is not None:
+        _dev(state_indices, "state_indices")
+        if state_indices.dtype != torch.int32 or state_indices.shape != (N,) or not state_indices.is_contiguous():
+            raise ValueError("state_indices must be a contiguous int32 [N] tensor")
+        idx = state_indices.data_ptr()
+    if o is None:
+        o = torch.empty((N, HV, Dv), dtype=torch.bfloat16, device=q.device)
+    ro = _heads(o, "o", v.shape, True)
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=q.device)
+    else:
+        _out(status, "status", (1,), _I32)
+    _check(lib().cconv_linattn_update(rq, rk, rv, log_decay.data_ptr(), scale, state.data_ptr(), state.shape[0], idx, ro,
+                                      N, H, HV, Dk, Dv, status.data_ptr(), _stream(stream)), "cconv_linattn_update")
+    return o, status
+
+
+def _norm_side(q, k, wq, wk, table, positions):
+    """The checks that both passes of the norm share: (rows of q, rows of k, weight dtype, P, R)."""
+    rq, rk = _heads(q, "q"), _heads(k, "k")
+    D = q.shape[3]
+    if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+        raise ValueError("k must have q's batch, rows and channels")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        _dev(w, name)
+        if w.dtype not in _WT or w.shape != (D,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 or fp32 [D] tensor")
+    if wq.dtype != wk.dtype:
+        raise ValueError("wq and wk must have one dtype")
+    P = R = 0
+    if table is not None:
+        _dev(table, "table")
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 [P, R] tensor")
+        P, R = table.shape
+    if positions is not None:
+        _dev(positions, "positions")
+        if positions.dtype != torch.int32 or positions.shape != q.shape[:2] or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 [B, T] tensor")
+    return rq, rk, (BF16 if wq.dtype == torch.bfloat16 else F32), P, R
+
+
+def cconv_qknorm_fwd(q, k, wq, wk, table=None, *, positions=None, eps: float = 1e-6, interleaved: bool = False, yq=None,
+                     yk=None, status=None, stream=None):
+    """The norm of every query and key head over its channels and the rotation of its first R channels
+    by the row's position, in one pass. Returns (yq, yk, status).
+
+    q, k: bf16 [B, T, H, D] (any strides with contiguous channels); wq, wk: [D]; table: fp32 [P, R],
+    R/2 cosines then R/2 sines of each position, or None (no rotation). Pairs are (c, c + R/2), or
+    with ``interleaved`` (2c, 2c + 1). positions: int32 [B, T], or None (row t is position t). With
+    positions and a table, status (a device int32, else None) receives 0, or 8 when a position lies
+    outside the table.
+    """
+    rq, rk, wdt, P, R = _norm_side(q, k, wq, wk, table, positions)
+    B, T, Hq, D = q.shape
+    if yq is None:
+        yq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if yk is None:
+        yk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    ryq, ryk = _heads(yq, "yq", q.shape), _heads(yk, "yk", k.shape)
+    pos = positions.data_ptr() if positions is not None and R else None
+    if pos is None:
+        status = None
+    elif status is None:
+        status = torch.empty(1, dtype=torch.int32, device=q.device)
+    else:
+        _out(status, "status", (1,), _I32)
+    _check(lib().cconv_qknorm_fwd(rq, rk, wq.data_ptr(), wk.data_ptr(), wdt, table.data_ptr() if R else None, P, R,
+                                  int(interleaved), pos, eps, ryq, ryk, B, T, Hq, k.shape[2], D,
+                                  None if status is None else status.data_ptr(), _stream(stream)), "cconv_qknorm_fwd")
+    return yq, yk, status
+
+
+def cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D) -> int:
+    return int(lib().cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D))
+
+
+def cconv_qknorm_bwd(q, k, dyq, dyk, wq, wk, table=None, *, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                     dq=None, dk=None, dwq=None, dwk=None, status=None, workspace=None, stream=None):
+    """Gradients of cconv_qknorm_fwd: returns (dq, dk, dwq, dwk, status); dwq and dwk have the
+    weights' dtype (sums over all rows and heads in fp32, in a fixed order)."""
+    rq, rk, wdt, P, R = _norm_side(q, k, wq, wk, table, positions)
+    B, T, Hq, D = q.shape
+    Hk, dev = k.shape[2], q.device
+    rdyq, rdyk = _heads(dyq, "dyq", q.shape), _heads(dyk, "dyk", k.shape)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    if dwq is None:
+        dwq = torch.empty(D, dtype=wq.dtype, device=dev)
+    if dwk is None:
+        dwk = torch.empty(D, dtype=wk.dtype, device=dev)
+    _out(dwq, "dwq", (D,), (wq.dtype,))
+    _out(dwk, "dwk", (D,), (wk.dtype,))
+    rdq, rdk = _heads(dq, "dq", q.shape), _heads(dk, "dk", k.shape)
+    pos = positions.data_ptr() if positions is not None and R else None
+    if pos is None:
+        status = None
+    elif status is None:
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        _out(status, "status", (1,), _I32)
+    L = lib()
+    workspace, ws_bytes = _workspace(workspace, L.cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D), dev)
+    _check(L.cconv_qknorm_bwd(rq, rk, rdyq, rdyk, wq.data_ptr(), wk.data_ptr(), wdt, table.data_ptr() if R else None, P, R,
+                              int(interleaved), pos, eps, rdq, rdk, dwq.data_ptr(), dwk.data_ptr(), _ptr(workspace),
+                              ws_bytes, B, T, Hq, Hk, D, None if status is None else status.data_ptr(), _stream(stream)),
+           "cconv_qknorm_bwd")
+    return dq, dk, dwq, dwk, status

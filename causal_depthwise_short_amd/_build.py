@@ -34,7 +34,7 @@ CFLAGS = [
 LIBS = {
     "libcconv.so": [
         "cconv_api.hip", "cconv_fwd.hip", "cconv_fwd_extra.hip", "cconv_bwd.hip", "cconv_bwd_extra.hip",
-        "cconv_update.hip", "cconv_seq.hip",
+        "cconv_update.hip", "cconv_seq.hip", "linattn_api.hip", "linattn_walk.hip", "linattn_update.hip", "qknorm.hip",
     ],
     "libcconv_roofline.so": ["roofline_copy.hip"],
 }

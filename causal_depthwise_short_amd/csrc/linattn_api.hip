@@ -1,0 +1,615 @@
+// linattn_api.hip -- host side of linear attention and of the per-head norm with rotation
+// (include/cconv.h): checks, the cut into segments, and the order of the launches. As everywhere in
+// the library, nothing here allocates device memory, synchronises or reads device memory, and every
+// check that can fail happens before the first launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/cconv.h"
+#include "cconv_internal.hpp"
+#include "linattn_internal.hpp"
+
+using namespace cconv;
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 40;    // any size times a stride stays far below 2^63
+constexpr int64_t kMaxRowCount = int64_t(1) << 31;  // rows of a packed batch (32-bit offsets)
+constexpr int64_t kMaxHeads = int64_t(1) << 16;
+constexpr int64_t kMaxHeadDim = 256;
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxSequences = int64_t(1) << 24;
+constexpr int64_t kMaxDecodeRows = int64_t(1) << 24;
+constexpr int64_t kMaxStepSlots = int64_t(1) << 18;  // the slot check's bits next to the step's own LDS
+// Segments: enough workgroups for two on each of the 256 CUs, each of at least kMinSegment rows (a
+// segment costs one more read of its k and v and two passes over its state).
+constexpr int64_t kTargetGroups = 512;
+constexpr int64_t kMinSegment = 256;
+constexpr int64_t kNormWaves = 4096;      // waves a norm wants before a wave takes several heads in turn
+constexpr int64_t kNormBwdBlocks = 1024;  // blocks of the norm's backward, each with one partial of dw
+
+struct Span {
+    uintptr_t lo, hi;
+};
+
+Span span(const void* p, __int128 bytes) {
+    if (!p || bytes <= 0) return {0, 0};
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + static_cast<uintptr_t>(bytes)};
+}
+
+bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// The operands of a call, for the check that no output overlaps anything else.
+struct Operands {
+    Span in[20], out[12];
+    int ins = 0, outs = 0;
+    void add_in(Span s) { in[ins++] = s; }
+    void add_out(Span s) { out[outs++] = s; }
+    bool clash() const {
+        for (int i = 0; i < outs; ++i) {
+            for (int j = 0; j < ins; ++j)
+                if (overlap(out[i], in[j])) return true;
+            for (int j = 0; j < i; ++j)
+                if (overlap(out[i], out[j])) return true;
+        }
+        return false;
+    }
+};
+
+struct Dims {
+    int64_t B, T, heads, dim;
+    bool empty() const { return B == 0 || T == 0; }
+};
+
+Span rows_span(const cconv_rows_t& r, const Dims& d) {
+    if (d.empty()) return {0, 0};
+    return span(r.p, (static_cast<__int128>(d.B - 1) * r.sb + static_cast<__int128>(d.T - 1) * r.st +
+                      static_cast<__int128>(d.heads - 1) * r.sh + d.dim) * 2);
+}
+
+// Strides in range; for an output also elements that do not overlap: taken from the smallest stride
+// up, each axis steps over all that lies inside it.
+cconv_status_t check_rows(const cconv_rows_t* r, const Dims& d, bool out) {
+    if (!r || (!r->p && !d.empty())) return CCONV_ERR_NULL_POINTER;
+    if (r->sb < 0 || r->st < 0 || r->sh < 0 || r->sb > kMaxDim || r->st > kMaxDim || r->sh > kMaxDim)
+        return CCONV_ERR_BAD_STRIDE;
+    if (!aligned(r->p, 2)) return CCONV_ERR_MISALIGNED;
+    if (out && !d.empty()) {
+        std::pair<int64_t, int64_t> ax[3] = {{r->sb, d.B}, {r->st, d.T}, {r->sh, d.heads}};
+        std::sort(ax, ax + 3);
+        __int128 extent = d.dim;
+        for (const auto& x : ax) {
+            if (x.second == 1) continue;
+            if (x.first < extent) return CCONV_ERR_BAD_STRIDE;
+            extent += static_cast<__int128>(x.second - 1) * x.first;
+        }
+    }
+    return CCONV_OK;
+}
+
+// Elements of a row that one load may take (an axis of length 1 has no stride that matters).
+int row_vec(const cconv_rows_t& r, const Dims& d) {
+    const int64_t s = (d.B > 1 ? r.sb : 0) | (d.T > 1 ? r.st : 0) | (d.heads > 1 ? r.sh : 0);
+    if (d.dim % 8 == 0 && s % 8 == 0 && aligned(r.p, 16)) return 8;
+    if (d.dim % 4 == 0 && s % 2 == 0 && aligned(r.p, 4)) return 4;
+    return 1;
+}
+
+Rows rows_of(const cconv_rows_t& r, const Dims& d, int hdiv) {
+    return Rows{static_cast<const uint16_t*>(r.p), r.sb, r.st, r.sh, hdiv, static_cast<int>(d.dim), row_vec(r, d)};
+}
+
+// ---- linear attention over sequences -------------------------------------------------------
+
+struct Cut {
+    int64_t nseq, seg_rows, segs, segments;
+};
+
+int64_t value_blocks(const WalkShape& w, int64_t Dv) { return (Dv + 4 * w.NV - 1) / (4 * w.NV); }
+
+// How sequences are cut into segments: `groups` workgroups take one segment.
+Cut cut_of(int64_t B, int64_t T, int64_t nseq, int64_t groups) {
+    Cut c;
+    const int64_t rows = B * T;
+    const int64_t want = std::max<int64_t>(1, kTargetGroups / std::max<int64_t>(1, groups));  // segments in all
+    const int64_t each = std::max<int64_t>(kMinSegment, (rows + want - 1) / want);
+    c.seg_rows = (each + kChunk - 1) / kChunk * kChunk;
+    if (nseq < 0) {
+        c.nseq = B;
+        c.segs = std::max<int64_t>(1, (T + c.seg_rows - 1) / c.seg_rows);
+        c.segments = B * c.segs;
+    } else {
+        c.nseq = nseq;
+        c.segs = T > c.seg_rows ? 2 : 1;  // whether any sequence may have more than one
+        c.segments = T / c.seg_rows + nseq;
+    }
+    return c;
+}
+
+int64_t state_floats(const WalkShape& w, int64_t Dv) { return w.DK * 4 * w.NV * value_blocks(w, Dv); }
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+struct Workspace {
+    size_t states = 0, plan = 0, part = 0;
+    size_t bytes() const { return states + plan + part; }
+};
+
+size_t plan_bytes(const Cut& c, int64_t nseq) {
+    return nseq < 0 ? 0 : align16((c.nseq + 1 + 2 * c.segments) * 4);
+}
+
+bool sizes_ok(int64_t B, int64_t T, int64_t nseq, int64_t H, int64_t HV, int64_t Dk, int64_t Dv) {
+    if (B < 0 || T < 0 || H < 1 || HV < 1 || HV % H != 0 || Dk < 1 || Dv < 1) return false;
+    if (HV > kMaxHeads || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return false;
+    if (nseq > kMaxSequences || B > kMaxSequences || T >= kMaxRowCount) return false;
+    return static_cast<__int128>(B) * T < (int64_t(1) << 40) &&
+           static_cast<__int128>(B) * T * HV * kMaxHeadDim * 4 < (static_cast<__int128>(1) << 62);
+}
+
+Workspace fwd_workspace(int64_t B, int64_t T, int64_t nseq, int64_t HV, int64_t Dk, int64_t Dv, Cut* cut) {
+    const WalkShape w = walk_shape(Dk, Dv);
+    *cut = cut_of(B, T, nseq, HV * value_blocks(w, Dv));
+    Workspace ws;
+    if (cut->segs > 1) ws.states = align16(cut->segments * HV * state_floats(w, Dv) * 4);
+    ws.plan = plan_bytes(*cut, nseq);
+    return ws;
+}
+
+Workspace bwd_workspace(int64_t B, int64_t T, int64_t nseq, int64_t H, int64_t HV, int64_t Dk, int64_t Dv, Cut* cut) {
+    const WalkShape kv = walk_shape(Dk, Dv), vk = walk_shape(Dv, Dk);
+    *cut = cut_of(B, T, nseq, HV * std::min(value_blocks(kv, Dv), value_blocks(vk, Dk)));
+    Workspace ws;
+    if (cut->segs > 1) ws.states = align16(cut->segments * HV * std::max(state_floats(kv, Dv), state_floats(vk, Dk)) * 4);
+    ws.plan = plan_bytes(*cut, nseq);
+    if (HV > H) ws.part = align16(B * T * HV * Dk * 4);
+    return ws;
+}
+
+bool grid_ok(const Cut& c, int64_t HV, int64_t Dk, int64_t Dv) {
+    const WalkShape w = walk_shape(Dk, Dv);
+    return static_cast<__int128>(c.segments) * HV * value_blocks(w, Dv) <= kMaxGrid &&
+           static_cast<__int128>(c.nseq) * HV * (state_floats(w, Dv) / 1024) <= kMaxGrid;
+}
+
+// Carves the workspace and, for packed batches, launches the check of the offsets.
+struct Prepared {
+    float* states;
+    int32_t *seq_seg, *seg_of;
+    float* part;
+};
+
+Prepared carve(void* workspace, const Workspace& ws, const Cut& c) {
+    char* p = static_cast<char*>(workspace);
+    Prepared r;
+    r.states = reinterpret_cast<float*>(p);
+    r.seq_seg = reinterpret_cast<int32_t*>(p + ws.states);
+    r.seg_of = r.seq_seg + c.nseq + 1;
+    r.part = reinterpret_cast<float*>(p + ws.states + ws.plan);
+    return r;
+}
+
+cconv_status_t walk(const WalkArgs& args, const Cut& c, const Prepared& p, hipStream_t s) {
+    WalkArgs a = args;
+    const WalkShape w = walk_shape(a.k.dim, a.v.dim);
+    a.vblocks = static_cast<int>(value_blocks(w, a.v.dim));
+    a.states = p.states;
+    a.seg_of = a.cu ? p.seg_of : nullptr;
+    a.seg_rows = c.seg_rows;
+    a.segs = c.segs;
+    a.segments = c.segments;
+    if (c.segs > 1) {
+        if (launch_walk(w, true, a, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+        ScanArgs sc;
+        sc.states = p.states;
+        sc.log_decay = a.log_decay;
+        sc.seq_seg = a.cu ? p.seq_seg : nullptr;
+        sc.status = a.status;
+        sc.seg_rows = c.seg_rows;
+        sc.segs = c.segs;
+        sc.nseq = c.nseq;
+        sc.floats = state_floats(w, a.v.dim);
+        sc.HV = a.HV;
+        if (launch_scan(sc, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+    }
+    return launch_walk(w, false, a, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+}
+
+// What the forward and the backward check alike. `n`: state rows.
+cconv_status_t check_sequences(const float* log_decay, float scale, const int32_t* cu, int64_t nseq, int32_t* status,
+                               int64_t B, int64_t T, int64_t H, int64_t HV, int64_t Dk, int64_t Dv) {
+    if (cu && (B != 1 || nseq < 0)) return CCONV_ERR_BAD_SHAPE;
+    if (cu && nseq == 0 && T > 0) return CCONV_ERR_BAD_SHAPE;
+    if (!sizes_ok(B, T, cu ? nseq : -1, H, HV, Dk, Dv)) return CCONV_ERR_BAD_SHAPE;
+    if (!log_decay || (cu && !status)) return CCONV_ERR_NULL_POINTER;
+    if (std::isnan(scale)) return CCONV_ERR_BAD_CONFIG;
+    if (!aligned(log_decay, 4) || !aligned(cu, 4) || !aligned(status, 4)) return CCONV_ERR_MISALIGNED;
+    return CCONV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cconv_linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t nseq, int64_t HV, int64_t Dk, int64_t Dv) {
+    if (!sizes_ok(B, T, nseq, 1, HV, Dk, Dv)) return 0;
+    Cut c;
+    return fwd_workspace(B, T, nseq < 0 ? -1 : nseq, HV, Dk, Dv, &c).bytes();
+}
+
+cconv_status_t cconv_linattn_fwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                 const float* log_decay, float scale, const float* init_state, const cconv_rows_t* o,
+                                 float* final_state, const int32_t* cu_seqlens, int64_t nseq, int32_t* status,
+                                 void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t HV,
+                                 int64_t Dk, int64_t Dv, cconv_stream_t stream) {
+    cconv_status_t st = check_sequences(log_decay, scale, cu_seqlens, nseq, status, B, T, H, HV, Dk, Dv);
+    if (st != CCONV_OK) return st;
+    const Dims dk{B, T, H, Dk}, dv{B, T, HV, Dv};
+    if ((st = check_rows(q, dk, false)) != CCONV_OK || (st = check_rows(k, dk, false)) != CCONV_OK ||
+        (st = check_rows(v, dv, false)) != CCONV_OK || (st = check_rows(o, dv, true)) != CCONV_OK)
+        return st;
+    if (!aligned(init_state, 4) || !aligned(final_state, 4) || !aligned(workspace, 16)) return CCONV_ERR_MISALIGNED;
+    Cut c;
+    const Workspace ws = fwd_workspace(B, T, cu_seqlens ? nseq : -1, HV, Dk, Dv, &c);
+    if (!grid_ok(c, HV, Dk, Dv)) return CCONV_ERR_BAD_SHAPE;
+    if (ws.bytes() > 0 && !workspace) return CCONV_ERR_NULL_POINTER;
+    if (workspace_bytes < ws.bytes()) return CCONV_ERR_WORKSPACE;
+    const __int128 state_bytes = static_cast<__int128>(c.nseq) * HV * Dk * Dv * 4;
+    Operands ops;
+    ops.add_in(rows_span(*q, dk));
+    ops.add_in(rows_span(*k, dk));
+    ops.add_in(rows_span(*v, dv));
+    ops.add_in(span(log_decay, HV * 4));
+    ops.add_in(span(init_state, state_bytes));
+    ops.add_in(span(cu_seqlens, (nseq + 1) * 4));
+    ops.add_out(rows_span(*o, dv));
+    ops.add_out(span(final_state, state_bytes));
+    ops.add_out(span(cu_seqlens ? status : nullptr, 4));
+    ops.add_out(span(workspace, ws.bytes()));
+    if (ops.clash()) return CCONV_ERR_ALIASING;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const Prepared p = carve(workspace, ws, c);
+    if (cu_seqlens && launch_seg_plan(cu_seqlens, nseq, T, c.seg_rows, status, p.seq_seg, p.seg_of, c.segments, s) != hipSuccess)
+        return CCONV_ERR_LAUNCH;
+    if (c.segments == 0) return CCONV_OK;
+
+    WalkArgs a{};
+    const int grp = static_cast<int>(HV / H);
+    a.q = rows_of(*q, dk, grp);
+    a.k = rows_of(*k, dk, grp);
+    a.v = rows_of(*v, dv, 1);
+    a.o = const_cast<void*>(o->p);
+    a.o_sb = o->sb, a.o_st = o->st, a.o_sh = o->sh;
+    a.o_vec = row_vec(*o, dv) >= 4 ? 4 : 1;
+    a.log_decay = log_decay;
+    a.alpha = a.beta = scale, a.gamma = 1.0f;
+    a.shift = 1;
+    a.init = init_state, a.fin = final_state;
+    a.sk = Dv, a.sv = 1;
+    a.cu = cu_seqlens, a.status = cu_seqlens ? status : nullptr;
+    a.T = T;
+    a.HV = static_cast<int>(HV);
+    return walk(a, c, p, s);
+}
+
+size_t cconv_linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t nseq, int64_t H, int64_t HV, int64_t Dk,
+                                         int64_t Dv) {
+    if (!sizes_ok(B, T, nseq, H, HV, Dk, Dv)) return 0;
+    Cut c;
+    return bwd_workspace(B, T, nseq < 0 ? -1 : nseq, H, HV, Dk, Dv, &c).bytes();
+}
+
+cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                 const float* log_decay, float scale, const float* init_state,
+                                 const cconv_rows_t* d_o, const float* d_final_state, const cconv_rows_t* dq,
+                                 const cconv_rows_t* dk, const cconv_rows_t* dv, float* d_init_state,
+                                 const int32_t* cu_seqlens, int64_t nseq, int32_t* status, void* workspace,
+                                 size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t HV, int64_t Dk,
+                                 int64_t Dv, cconv_stream_t stream) {
+    cconv_status_t st = check_sequences(log_decay, scale, cu_seqlens, nseq, status, B, T, H, HV, Dk, Dv);
+    if (st != CCONV_OK) return st;
+    const Dims nk{B, T, H, Dk}, nv{B, T, HV, Dv};
+    const cconv_rows_t* in[4] = {q, k, v, d_o};
+    const cconv_rows_t* out[3] = {dq, dk, dv};
+    for (int i = 0; i < 4; ++i)
+        if ((st = check_rows(in[i], i < 2 ? nk : nv, false)) != CCONV_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if ((st = check_rows(out[i], i < 2 ? nk : nv, true)) != CCONV_OK) return st;
+    if (!aligned(init_state, 4) || !aligned(d_final_state, 4) || !aligned(d_init_state, 4) || !aligned(workspace, 16))
+        return CCONV_ERR_MISALIGNED;
+    Cut c;
+    const Workspace ws = bwd_workspace(B, T, cu_seqlens ? nseq : -1, H, HV, Dk, Dv, &c);
+    if (!grid_ok(c, HV, Dk, Dv) || !grid_ok(c, HV, Dv, Dk)) return CCONV_ERR_BAD_SHAPE;
+    if (ws.bytes() > 0 && !workspace) return CCONV_ERR_NULL_POINTER;
+    if (workspace_bytes < ws.bytes()) return CCONV_ERR_WORKSPACE;
+    const __int128 state_bytes = static_cast<__int128>(c.nseq) * HV * Dk * Dv * 4;
+    Operands ops;
+    for (int i = 0; i < 4; ++i) ops.add_in(rows_span(*in[i], i < 2 ? nk : nv));
+    ops.add_in(span(log_decay, HV * 4));
+    ops.add_in(span(init_state, state_bytes));
+    ops.add_in(span(d_final_state, state_bytes));
+    ops.add_in(span(cu_seqlens, (nseq + 1) * 4));
+    for (int i = 0; i < 3; ++i) ops.add_out(rows_span(*out[i], i < 2 ? nk : nv));
+    ops.add_out(span(d_init_state, state_bytes));
+    ops.add_out(span(cu_seqlens ? status : nullptr, 4));
+    ops.add_out(span(workspace, ws.bytes()));
+    if (ops.clash()) return CCONV_ERR_ALIASING;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const Prepared p = carve(workspace, ws, c);
+    if (cu_seqlens && launch_seg_plan(cu_seqlens, nseq, T, c.seg_rows, status, p.seq_seg, p.seg_of, c.segments, s) != hipSuccess)
+        return CCONV_ERR_LAUNCH;
+    if (c.segments == 0) return CCONV_OK;
+
+    const int grp = static_cast<int>(HV / H);
+    const Rows rq = rows_of(*q, nk, grp), rk = rows_of(*k, nk, grp), rv = rows_of(*v, nv, 1), rdo = rows_of(*d_o, nv, 1);
+    WalkArgs base{};
+    base.log_decay = log_decay;
+    base.cu = cu_seqlens, base.status = cu_seqlens ? status : nullptr;
+    base.T = T;
+    base.HV = static_cast<int>(HV);
+    // an output shared by a group's value heads is summed from fp32 rows of each
+    auto to = [&](WalkArgs& a, const cconv_rows_t& r, const Dims& d) {
+        if (d.heads == HV) {
+            a.o = const_cast<void*>(r.p);
+            a.o_sb = r.sb, a.o_st = r.st, a.o_sh = r.sh;
+            a.o_f32 = 0;
+            a.o_vec = row_vec(r, d) >= 4 ? 4 : 1;
+        } else {
+            a.o = p.part;
+            a.o_sh = d.dim, a.o_st = HV * d.dim, a.o_sb = T * a.o_st;
+            a.o_f32 = 1;
+            a.o_vec = d.dim % 4 == 0 ? 4 : 1;
+        }
+    };
+    auto sum = [&](const cconv_rows_t& r) {
+        if (HV == H || B * T == 0) return CCONV_OK;
+        GroupSumArgs g;
+        g.part = p.part;
+        g.out = static_cast<uint16_t*>(const_cast<void*>(r.p));
+        g.o_sb = r.sb, g.o_st = r.st, g.o_sh = r.sh;
+        g.B = B, g.T = T;
+        g.H = static_cast<int>(H), g.grp = grp, g.dim = static_cast<int>(Dk);
+        g.status = base.status;
+        return launch_group_sum(g, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+    };
+
+    // dq: forwards, the state transposed (values are its keys)
+    WalkArgs a = base;
+    a.q = rdo, a.k = rv, a.v = rk;
+    a.alpha = a.beta = scale, a.gamma = 1.0f;
+    a.shift = 1;
+    a.init = init_state;
+    a.sk = 1, a.sv = Dv;
+    to(a, *dq, nk);
+    if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dq)) != CCONV_OK) return st;
+    // dk and dv: backwards, carrying the gradient of the state
+    a = base;
+    a.q = rv, a.k = rdo, a.v = rq;
+    a.alpha = scale, a.beta = 1.0f, a.gamma = scale;
+    a.shift = 0, a.reverse = 1;
+    a.init = d_final_state;
+    a.sk = 1, a.sv = Dv;
+    to(a, *dk, nk);
+    if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dk)) != CCONV_OK) return st;
+    a.q = rk, a.k = rq, a.v = rdo;
+    a.fin = d_init_state;
+    a.sk = Dv, a.sv = 1;
+    to(a, *dv, nv);
+    return walk(a, c, p, s);
+}
+
+cconv_status_t cconv_linattn_update(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                    const float* log_decay, float scale, float* state, int64_t S,
+                                    const int32_t* state_indices, const cconv_rows_t* o, int64_t N, int64_t H,
+                                    int64_t HV, int64_t Dk, int64_t Dv, int32_t* status, cconv_stream_t stream) {
+    if (N < 0 || S < 0 || N > kMaxDecodeRows || S > kMaxDim || !sizes_ok(1, N, -1, H, HV, Dk, Dv)) return CCONV_ERR_BAD_SHAPE;
+    if (state_indices && S > kMaxStepSlots) return CCONV_ERR_BAD_SHAPE;
+    if (!state_indices && N > S) return CCONV_ERR_BAD_SHAPE;
+    if (!log_decay || (!state && S > 0)) return CCONV_ERR_NULL_POINTER;
+    if (state_indices && !status && N > 0) return CCONV_ERR_NULL_POINTER;
+    if (std::isnan(scale)) return CCONV_ERR_BAD_CONFIG;
+    const Dims dk{1, N, H, Dk}, dv{1, N, HV, Dv};
+    cconv_status_t st;
+    if ((st = check_rows(q, dk, false)) != CCONV_OK || (st = check_rows(k, dk, false)) != CCONV_OK ||
+        (st = check_rows(v, dv, false)) != CCONV_OK || (st = check_rows(o, dv, true)) != CCONV_OK)
+        return st;
+    if (!aligned(log_decay, 4) || !aligned(state, 4) || !aligned(state_indices, 4) || !aligned(status, 4))
+        return CCONV_ERR_MISALIGNED;
+    if (static_cast<__int128>(N) * HV * 16 > kMaxGrid) return CCONV_ERR_BAD_SHAPE;
+    const __int128 state_bytes = static_cast<__int128>(S) * HV * Dk * Dv * 4;
+    Operands ops;
+    ops.add_in(rows_span(*q, dk));
+    ops.add_in(rows_span(*k, dk));
+    ops.add_in(rows_span(*v, dv));
+    ops.add_in(span(log_decay, HV * 4));
+    ops.add_in(span(state_indices, N * 4));
+    ops.add_out(rows_span(*o, dv));
+    ops.add_out(span(state, state_bytes));
+    ops.add_out(span(status, 4));
+    if (ops.clash()) return CCONV_ERR_ALIASING;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (N == 0) return !status || launch_status(status, CCONV_OK, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+    StepArgs a;
+    const int grp = static_cast<int>(HV / H);
+    a.q = rows_of(*q, dk, grp);
+    a.k = rows_of(*k, dk, grp);
+    a.v = rows_of(*v, dv, 1);
+    a.log_decay = log_decay;
+    a.scale = scale;
+    a.pool = state;
+    a.idx = state_indices;
+    a.o = static_cast<uint16_t*>(const_cast<void*>(o->p));
+    a.o_st = o->st, a.o_sh = o->sh;
+    a.N = N, a.S = S;
+    a.HV = static_cast<int>(HV), a.Dk = static_cast<int>(Dk), a.Dv = static_cast<int>(Dv);
+    a.status = status;
+    return launch_step(a, Dv % 4 == 0 && aligned(state, 16), s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+}
+
+// ---- the per-head norm with rotation -------------------------------------------------------
+
+namespace {
+
+struct NormCall {
+    const cconv_rows_t *q, *k, *dyq, *dyk, *oq, *ok;  // o: outputs (yq, yk, or dq, dk)
+    const void *wq, *wk;
+    cconv_dtype_t w_dtype;
+    const float* table;
+    int64_t P, R;
+    int interleaved;
+    const int32_t* pos;
+    float eps;
+    void *dwq, *dwk;
+    void* workspace;
+    size_t workspace_bytes;
+    int64_t B, T, Hq, Hk, D;
+    int32_t* status;
+    bool bwd;
+};
+
+// Channel pairs a lane takes: both members' loads are whole and aligned to 4 bytes.
+int norm_vec(const NormCall& c, const cconv_rows_t* const* rows, const Dims* dims, int n) {
+    bool even = true;
+    for (int i = 0; i < n; ++i) even = even && row_vec(*rows[i], Dims{dims[i].B, dims[i].T, dims[i].heads, 4}) >= 4;
+    if (!even) return 1;
+    if (c.interleaved) return c.D % 8 == 0 ? 4 : c.D % 4 == 0 ? 2 : 1;
+    if (c.R % 8 == 0 && c.D % 8 == 0) return 4;
+    return c.R % 4 == 0 && c.D % 4 == 0 ? 2 : 1;
+}
+
+int64_t norm_blocks(int64_t B, int64_t T, int64_t chunks) {
+    return std::max<int64_t>(1, std::min<int64_t>(kNormBwdBlocks, (B * T * chunks + 3) / 4));
+}
+
+size_t norm_ws(int64_t B, int64_t T, int64_t D) {
+    (void)B, (void)T;
+    return static_cast<size_t>(kNormBwdBlocks) * 2 * D * 4;
+}
+
+cconv_status_t norm_impl(NormCall c, hipStream_t s) {
+    if (c.B < 0 || c.T < 0 || c.Hq < 1 || c.Hk < 1 || c.D < 1 || c.D > kMaxHeadDim || c.Hq > kMaxHeads || c.Hk > kMaxHeads ||
+        c.P < 0 || c.P > kMaxRowCount || c.R < 0 || c.R % 2 != 0 || c.R > c.D || c.B > kMaxSequences || c.T >= kMaxRowCount)
+        return CCONV_ERR_BAD_SHAPE;
+    const __int128 rows = static_cast<__int128>(c.B) * c.T;
+    if (rows > (static_cast<__int128>(1) << 32)) return CCONV_ERR_BAD_SHAPE;
+    if (c.w_dtype != CCONV_BF16 && c.w_dtype != CCONV_F32) return CCONV_ERR_UNSUPPORTED_DTYPE;
+    if (!c.wq || !c.wk || (c.R > 0 && !c.table && c.P > 0) || (c.pos && !c.status)) return CCONV_ERR_NULL_POINTER;
+    if (c.R > 0 && !c.pos && rows > 0 && c.T > c.P) return CCONV_ERR_BAD_SHAPE;
+    if (!(c.eps >= 0.0f) || (c.interleaved != 0 && c.interleaved != 1)) return CCONV_ERR_BAD_CONFIG;
+    const Dims dq{c.B, c.T, c.Hq, c.D}, dk{c.B, c.T, c.Hk, c.D};
+    const cconv_rows_t* all[6] = {c.q, c.k, c.oq, c.ok, c.dyq, c.dyk};
+    const Dims dims[6] = {dq, dk, dq, dk, dq, dk};
+    const int n = c.bwd ? 6 : 4;
+    cconv_status_t st;
+    for (int i = 0; i < n; ++i)
+        if ((st = check_rows(all[i], dims[i], i == 2 || i == 3)) != CCONV_OK) return st;
+    const uintptr_t we = c.w_dtype == CCONV_F32 ? 4 : 2;
+    if (!aligned(c.wq, we) || !aligned(c.wk, we) || !aligned(c.dwq, we) || !aligned(c.dwk, we) || !aligned(c.table, 4) ||
+        !aligned(c.pos, 4) || !aligned(c.status, 4) || !aligned(c.workspace, 16))
+        return CCONV_ERR_MISALIGNED;
+    if (c.bwd) {
+        if (!c.dwq || !c.dwk || !c.workspace) return CCONV_ERR_NULL_POINTER;
+        if (c.workspace_bytes < norm_ws(c.B, c.T, c.D)) return CCONV_ERR_WORKSPACE;
+    }
+    Operands ops;
+    for (int i = 0; i < n; ++i) {
+        const Span sp = rows_span(*all[i], dims[i]);
+        if (i == 2 || i == 3)
+            ops.add_out(sp);
+        else
+            ops.add_in(sp);
+    }
+    ops.add_in(span(c.wq, c.D * we));
+    ops.add_in(span(c.wk, c.D * we));
+    ops.add_in(span(c.table, static_cast<__int128>(c.P) * c.R * 4));
+    ops.add_in(span(c.pos, rows * 4));
+    ops.add_out(span(c.status, 4));
+    if (c.bwd) {
+        ops.add_out(span(c.dwq, c.D * we));
+        ops.add_out(span(c.dwk, c.D * we));
+        ops.add_out(span(c.workspace, norm_ws(c.B, c.T, c.D)));
+    }
+    if (ops.clash()) return CCONV_ERR_ALIASING;
+
+    NormArgs a{};
+    auto side = [&](const cconv_rows_t* x, const cconv_rows_t* dy, const cconv_rows_t* o, const void* w, int64_t heads) {
+        HeadRows h{};
+        h.x = static_cast<const uint16_t*>(x->p);
+        h.sb = x->sb, h.st = x->st, h.sh = x->sh;
+        if (dy) {
+            h.dy = static_cast<const uint16_t*>(dy->p);
+            h.dsb = dy->sb, h.dst = dy->st, h.dsh = dy->sh;
+        }
+        h.y = static_cast<uint16_t*>(const_cast<void*>(o->p));
+        h.ysb = o->sb, h.yst = o->st, h.ysh = o->sh;
+        h.w = w;
+        h.heads = static_cast<int>(heads);
+        return h;
+    };
+    a.q = side(c.q, c.bwd ? c.dyq : nullptr, c.oq, c.wq, c.Hq);
+    a.k = side(c.k, c.bwd ? c.dyk : nullptr, c.ok, c.wk, c.Hk);
+    a.table = c.table;
+    a.pos = c.pos;
+    a.P = c.P;
+    a.w_f32 = c.w_dtype == CCONV_F32;
+    a.D = static_cast<int>(c.D), a.R = static_cast<int>(c.R);
+    a.eps = c.eps;
+    a.B = c.B, a.T = c.T;
+    // one wave per row and side while that fills the chip; fewer heads a wave otherwise
+    if (c.R == 0) a.pos = c.pos = nullptr;  // nothing is rotated: positions are not read
+    a.status = c.pos ? c.status : nullptr;
+    const int64_t most = std::max(c.Hq, c.Hk), r = static_cast<int64_t>(rows);
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(most, kNormWaves / std::max<int64_t>(1, 2 * r)));
+    a.head_chunk = (most + split - 1) / split;
+    a.chunks = (c.Hq + a.head_chunk - 1) / a.head_chunk + (c.Hk + a.head_chunk - 1) / a.head_chunk;
+    if (static_cast<__int128>(r) * a.chunks / 4 > kMaxGrid) return CCONV_ERR_BAD_SHAPE;
+    a.blocks = norm_blocks(c.B, c.T, a.chunks);
+    if (!c.pos && c.status && launch_status(c.status, CCONV_OK, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+    a.part = static_cast<float*>(c.workspace);
+    if (rows == 0 && !c.bwd) {
+        if (c.pos && launch_status(c.status, CCONV_OK, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+        return CCONV_OK;
+    }
+    if (c.pos && launch_positions(c.pos, r, c.P, c.status, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+    const int vec = norm_vec(c, all, dims, n);
+    if (!c.bwd) return launch_qknorm_fwd(a, vec, c.interleaved, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+    if (launch_qknorm_bwd(a, vec, c.interleaved, s) != hipSuccess) return CCONV_ERR_LAUNCH;
+    return launch_qknorm_dw(a.part, a.blocks, a.D, c.dwq, c.dwk, a.w_f32, a.status, s) == hipSuccess ? CCONV_OK
+                                                                                                   : CCONV_ERR_LAUNCH;
+}
+
+}  // namespace
+
+cconv_status_t cconv_qknorm_fwd(const cconv_rows_t* q, const cconv_rows_t* k, const void* wq, const void* wk,
+                                cconv_dtype_t w_dtype, const float* table, int64_t P, int64_t R, int interleaved,
+                                const int32_t* positions, float eps, const cconv_rows_t* yq, const cconv_rows_t* yk,
+                                int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int32_t* status,
+                                cconv_stream_t stream) {
+    const NormCall c{q,   k,       nullptr, nullptr, yq,      yk, wq, wk, w_dtype, table, P, R,      interleaved, positions,
+                     eps, nullptr, nullptr, nullptr, 0,       B,  T,  Hq, Hk,      D,     status, false};
+    return norm_impl(c, reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t cconv_qknorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
+    if (B < 0 || T < 0 || Hq < 1 || Hk < 1 || D < 1 || D > kMaxHeadDim) return 0;
+    return norm_ws(B, T, D);
+}
+
+cconv_status_t cconv_qknorm_bwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* dyq,
+                                const cconv_rows_t* dyk, const void* wq, const void* wk, cconv_dtype_t w_dtype,
+                                const float* table, int64_t P, int64_t R, int interleaved, const int32_t* positions,
+                                float eps, const cconv_rows_t* dq, const cconv_rows_t* dk, void* dwq, void* dwk,
+                                void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t Hq, int64_t Hk,
+                                int64_t D, int32_t* status, cconv_stream_t stream) {
+    const NormCall c{q,   k,   dyq, dyk,       dq,              dk, wq, wk, w_dtype, table, P,      R,   interleaved, positions,
+                     eps, dwq, dwk, workspace, workspace_bytes, B,  T,  Hq, Hk,      D,     status, true};
+    return norm_impl(c, reinterpret_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,133 @@
+// linattn_internal.hpp -- argument structs and launchers shared by the host checks
+// (linattn_api.hip) and the kernels of linear attention (linattn_walk.hip, linattn_update.hip)
+// and of the per-head norm with rotation (qknorm.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace cconv {
+
+constexpr int kChunk = 64;  // rows of one chunk of the walk
+
+// One bf16 operand of a walk: element (b, t, head, c) at p + b*sb + t*st + (head / hdiv)*sh + c,
+// where head is the value head the workgroup works on.
+struct Rows {
+    const uint16_t* p;
+    int64_t sb, st, sh;
+    int hdiv;
+    int dim;   // channels
+    int vec;   // elements a load may take at once: 8 (16-byte aligned rows), 4 (4-byte) or 1
+};
+
+// One walk over the rows of every sequence (forwards or, with `reverse`, backwards), for each
+// value head with decay a = exp(log_decay):
+//   out_r  = alpha * sum_{j <= r} a^(r-j) (q_r . k_j) v_j + beta * a^(r+shift) q_r S
+//   S_next = a^n S + gamma * sum_j a^(n-shift-j) k_j^T v_j              (n rows of a chunk)
+// `segs` consecutive segments of seg_rows rows (a multiple of kChunk) of one sequence run in
+// workgroups of their own; `states` then carries S from one to the next.
+struct WalkArgs {
+    Rows q, k, v;
+    void* o;  // bf16 rows, or fp32 (o_f32)
+    int64_t o_sb, o_st, o_sh;
+    int o_f32, o_vec;
+    const float* log_decay;  // [HV]
+    float alpha, beta, gamma;
+    int shift, reverse;
+    const float* init;  // S before the first row of each sequence, or null (zeros)
+    float* fin;         // S after the last row, or null
+    int64_t sk, sv;     // strides of init and fin over the state's two axes; a head's matrix has Dk*Dv entries
+    float* states;      // [segments, HV, vblocks, DK*DVB]: per segment its own sum, then (scan) its carry-in
+    // packed batches: row offsets, and per segment its sequence and first row (see SegPlan)
+    const int32_t* cu;
+    const int32_t* seg_of;
+    const int32_t* status;
+    int64_t T, seg_rows;
+    int64_t segs;      // fixed lengths: segments of each sequence
+    int64_t segments;  // of the whole call (packed: at most)
+    int HV, vblocks;
+};
+
+// The tile a walk runs with: the key side padded to DK channels, the value side cut into
+// blocks of 4 * NV channels.
+struct WalkShape {
+    int DK, NV;
+};
+WalkShape walk_shape(int64_t Dk, int64_t Dv);
+
+hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, hipStream_t s);
+
+// Carry-in of every segment after a sequence's first: states[seg] becomes the sum that enters
+// segment seg + 1. `seq_seg` (packed): first segment of each sequence, nseq + 1 entries.
+struct ScanArgs {
+    float* states;
+    const float* log_decay;
+    const int32_t* seq_seg;
+    const int32_t* status;
+    int64_t seg_rows, segs, nseq, floats;  // floats: per (segment, head), all value blocks
+    int HV;
+};
+hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
+
+// Packed batches: checks the offsets (verdict to *status), and when they are good writes each
+// sequence's first segment and each segment's sequence. Empty sequences get one segment without rows.
+hipError_t launch_seg_plan(const int32_t* cu, int64_t nseq, int64_t total, int64_t seg_rows, int32_t* status,
+                           int32_t* seq_seg, int32_t* seg_of, int64_t segments, hipStream_t s);
+
+// out[row, h, c] = bf16 of the sum over the group's fp32 partials part[row, h*grp + g, c].
+struct GroupSumArgs {
+    const float* part;
+    uint16_t* out;
+    int64_t o_sb, o_st, o_sh;
+    int64_t B, T;
+    int H, grp, dim;
+    const int32_t* status;
+};
+hipError_t launch_group_sum(const GroupSumArgs& a, hipStream_t s);
+
+// One token for each of N rows: pool slot i = idx[n]: S = a S + k^T v, o = scale * q S.
+struct StepArgs {
+    Rows q, k, v;  // st: stride over n
+    const float* log_decay;
+    float scale;
+    float* pool;  // [S, HV, Dk, Dv]
+    const int32_t* idx;
+    uint16_t* o;
+    int64_t o_st, o_sh;
+    int64_t N, S;
+    int HV, Dk, Dv;
+    int32_t* status;
+};
+hipError_t launch_step(const StepArgs& a, bool vec4, hipStream_t s);
+
+// Per-head norm and rotation of q and k.
+struct HeadRows {
+    const uint16_t* x;
+    int64_t sb, st, sh;
+    const uint16_t* dy;  // backward
+    int64_t dsb, dst, dsh;
+    uint16_t* y;  // forward: the output; backward: dx
+    int64_t ysb, yst, ysh;
+    const void* w;
+    int heads;
+};
+struct NormArgs {
+    HeadRows q, k;
+    const float* table;  // [P, R]: R/2 cosines, R/2 sines
+    const int32_t* pos;  // [B, T] or null (row t is position t)
+    int64_t P;
+    int w_f32, D, R;
+    float eps;
+    int64_t B, T;
+    int64_t head_chunk, chunks;  // heads (of q, then k) a wave takes, and chunks of a row
+    const int32_t* status;       // checked before the call's first write
+    float* part;                 // backward: [blocks, 2, D]
+    int64_t blocks;
+};
+hipError_t launch_positions(const int32_t* pos, int64_t n, int64_t P, int32_t* status, hipStream_t s);
+hipError_t launch_qknorm_fwd(const NormArgs& a, int vec, bool interleaved, hipStream_t s);
+hipError_t launch_qknorm_bwd(const NormArgs& a, int vec, bool interleaved, hipStream_t s);
+hipError_t launch_qknorm_dw(const float* part, int64_t blocks, int D, void* dwq, void* dwk, int w_f32,
+                            const int32_t* status, hipStream_t s);
+
+}  // namespace cconv

@@ -1,0 +1,149 @@
+// linattn_update.hip -- linear attention for single tokens: one recurrent step of every row of a
+// decoding batch on a pool of fp32 states, S = a S + k^T v, o = scale * q S.
+//
+// The state is read once and written once; at 8 bytes and 5 operations an entry the step is bound
+// by that traffic. A thread owns VEC neighbouring value channels of every (256 / CL)-th key, so a
+// wave's loads and stores cover whole rows, and the first kRows rows' loads are in flight before
+// the slot check and the operands' loads are waited for. The partial sums of o over the keys meet in
+// LDS and are added in a fixed order.
+#include "../../include/cconv.h"
+#include "cconv_device.hpp"
+#include "linattn_internal.hpp"
+
+namespace cconv {
+
+namespace {
+
+constexpr int kStepThreads = 256;
+constexpr int kMaxKeys = 256;
+constexpr int kRows = 16;  // state rows of a thread in flight
+
+template <int VEC>
+struct Vec {
+    float f[VEC];
+};
+
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> load_state(const float* p) {
+    Vec<VEC> v;
+    if constexpr (VEC == 4) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        const f4 x = *reinterpret_cast<const f4*>(p);
+        v.f[0] = x.x, v.f[1] = x.y, v.f[2] = x.z, v.f[3] = x.w;
+    } else {
+        v.f[0] = *p;
+    }
+    return v;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_state(float* p, const Vec<VEC>& v) {
+    if constexpr (VEC == 4) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<f4*>(p) = f4{v.f[0], v.f[1], v.f[2], v.f[3]};
+    } else {
+        *p = v.f[0];
+    }
+}
+
+}  // namespace
+
+template <int VEC, int CL>
+__global__ __launch_bounds__(kStepThreads) void cconv_linattn_step_kernel(StepArgs a, int cblocks) {
+    constexpr int RG = kStepThreads / CL;
+    __shared__ float lq[kMaxKeys], lk[kMaxKeys];
+    __shared__ float part[RG][CL * VEC];
+    extern __shared__ uint32_t seen[];
+    const int64_t tile = blockIdx.x;
+    const int cb = static_cast<int>(tile % cblocks);
+    const int hv = static_cast<int>(tile / cblocks % a.HV);
+    const int64_t n = tile / (static_cast<int64_t>(cblocks) * a.HV);
+    const int tid = threadIdx.x, cl = tid % CL, rg = tid / CL;
+
+    SlotEntry first = {-1, 0};
+    if (a.idx && tid < a.N) first.v = a.idx[tid];
+    const int64_t slot = a.idx ? a.idx[n] : n;
+    const bool live = slot >= 0 && slot < a.S;
+    const int c0 = cb * CL * VEC + cl * VEC;
+    const bool mine = live && c0 < a.Dv;
+    float* S = a.pool + ((live ? slot : 0) * a.HV + hv) * static_cast<int64_t>(a.Dk) * a.Dv + c0;
+
+    Vec<VEC> s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * RG;
+        if (mine && r < a.Dk) s[i] = load_state<VEC>(S + static_cast<int64_t>(r) * a.Dv);
+    }
+    const uint16_t* qp = a.q.p + n * a.q.st + (hv / a.q.hdiv) * a.q.sh;
+    const uint16_t* kp = a.k.p + n * a.k.st + (hv / a.k.hdiv) * a.k.sh;
+    const uint16_t* vp = a.v.p + n * a.v.st + hv * a.v.sh;
+    for (int i = tid; i < a.Dk; i += kStepThreads) {
+        lq[i] = bf16_lo(qp[i]);
+        lk[i] = bf16_lo(kp[i]);
+    }
+    float v[VEC], o[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+        v[c] = c0 + c < a.Dv ? bf16_lo(vp[c0 + c]) : 0.0f;
+        o[c] = 0.0f;
+    }
+    const float decay = __builtin_amdgcn_exp2f(a.log_decay[hv] * 1.4426950408889634f);
+    if (a.idx) {
+        const bool bad = block_slots_bad(a.idx, nullptr, a.N, a.S, seen, first);
+        if (tile == 0 && tid == 0) *a.status = bad ? CCONV_ERR_INDEX : CCONV_OK;
+        if (bad) return;
+    } else if (a.status && tile == 0 && tid == 0) {
+        *a.status = CCONV_OK;
+    }
+    __syncthreads();
+
+    for (int r0 = 0; r0 < a.Dk; r0 += kRows * RG) {
+        if (r0 > 0) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + rg + i * RG;
+                if (mine && r < a.Dk) s[i] = load_state<VEC>(S + static_cast<int64_t>(r) * a.Dv);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + rg + i * RG;
+            if (!mine || r >= a.Dk) continue;
+            const float kr = lk[r], qr = lq[r];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                s[i].f[c] = __builtin_fmaf(decay, s[i].f[c], kr * v[c]);
+                o[c] = __builtin_fmaf(qr, s[i].f[c], o[c]);
+            }
+            store_state<VEC>(S + static_cast<int64_t>(r) * a.Dv, s[i]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) part[rg][cl * VEC + c] = o[c];
+    __syncthreads();
+    if (tid < CL * VEC) {
+        const int c = cb * CL * VEC + tid;
+        float t = part[0][tid];
+#pragma unroll
+        for (int r = 1; r < RG; ++r) t += part[r][tid];
+        if (c < a.Dv) a.o[n * a.o_st + hv * a.o_sh + c] = static_cast<uint16_t>(pack_bf16x2(live ? a.scale * t : 0.0f, 0.0f) & 0xffffu);
+    }
+}
+
+template <int VEC, int CL>
+static hipError_t step_go(const StepArgs& a, hipStream_t s) {
+    const int cblocks = (a.Dv + CL * VEC - 1) / (CL * VEC);
+    const size_t lds = a.idx ? ((a.S + 31) / 32 + 1) * 4 : 4;
+    hipLaunchKernelGGL((cconv_linattn_step_kernel<VEC, CL>), dim3(static_cast<uint32_t>(a.N * a.HV * cblocks)),
+                       dim3(kStepThreads), lds, s, a, cblocks);
+    return hipGetLastError();
+}
+
+hipError_t launch_step(const StepArgs& a, bool vec4, hipStream_t s) {
+    // few rows: narrower column blocks, so that more of the chip takes part
+    const bool few = a.N * a.HV < 256;
+    if (vec4) return few ? step_go<4, 8>(a, s) : step_go<4, 32>(a, s);
+    return few ? step_go<1, 16>(a, s) : step_go<1, 64>(a, s);
+}
+
+}  // namespace cconv

@@ -1,0 +1,455 @@
+// qknorm.hip -- the norm of every query and key head and the position rotation, in one pass:
+//     u = x / sqrt(mean(x^2) + eps) * w,  y = u with its first R channels rotated in pairs
+// by the angle of the row's position, and the gradients of x and w.
+//
+// Bound by memory: x is read once and y written once (backward: x and dy read, dx written). A head
+// is spread over G lanes (a power of two), VP channel pairs a lane, so that both channels of
+// a rotated pair sit in one lane, and 64 / G heads of a row go through a wave at once. The cosines
+// and sines of a row and the weights are loaded once for all of a wave's heads. Pairs are (p, p + R/2)
+// of the first R channels, or (2p, 2p+1); the channels past R are dealt out in pairs the same way
+// and not rotated.
+#include "../../include/cconv.h"
+#include "cconv_device.hpp"
+#include "linattn_internal.hpp"
+
+namespace cconv {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int64_t kOwnCheck = 1024;  // at most this many positions: every block checks all of them
+
+typedef unsigned int u32x4a __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x4n __attribute__((ext_vector_type(4)));
+
+// Where a lane's pairs lie in a head. `ca`, `cb`: first channel of the pairs' first and second
+// members (stride 1 between pairs, or 2 when interleaved); na, nb: how many of them exist.
+template <int VP, bool INTER>
+struct Place {
+    int ca, cb, na, nb, p0;
+    __device__ __forceinline__ Place(int lane_pair, int D, int R) {
+        p0 = lane_pair;
+        if constexpr (INTER) {
+            ca = 2 * p0, cb = ca + 1;
+            na = clampn((D - ca + 1) / 2), nb = clampn((D - ca) / 2);
+        } else {
+            const int half = R / 2, rest = D - R, rhalf = (rest + 1) / 2;
+            if (p0 < half) {
+                ca = p0, cb = p0 + half;
+                na = nb = clampn(half - p0);
+            } else {
+                const int q = p0 - half;
+                ca = R + q, cb = ca + rhalf;
+                na = clampn(rhalf - q), nb = clampn(rest - rhalf - q);
+            }
+        }
+    }
+    static __device__ __forceinline__ int clampn(int n) { return n < 0 ? 0 : n > VP ? VP : n; }
+};
+
+// N consecutive elements, all present (N = 8, 4, 2) or one.
+template <int N>
+__device__ __forceinline__ void load_n(const uint16_t* p, float (&f)[N]) {
+    if constexpr (N == 8) {
+        const u32x4a v = *reinterpret_cast<const u32x4a*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
+    } else if constexpr (N == 4) {
+        const u32x2a v = *reinterpret_cast<const u32x2a*>(p);
+        f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+    } else if constexpr (N == 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+        f[0] = bf16_lo(v), f[1] = bf16_hi(v);
+    } else {
+        f[0] = bf16_lo(*p);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_n(uint16_t* p, const float (&f)[N]) {
+    if constexpr (N == 8) {
+        u32x4a v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        *reinterpret_cast<u32x4a*>(p) = v;
+    } else if constexpr (N == 4) {
+        u32x2a v;
+        v.x = pack_bf16x2(f[0], f[1]), v.y = pack_bf16x2(f[2], f[3]);
+        *reinterpret_cast<u32x2a*>(p) = v;
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
+    } else {
+        *p = static_cast<uint16_t>(pack_bf16x2(f[0], 0.0f) & 0xffffu);
+    }
+}
+
+// A lane's pairs of one head: x[0][i], x[1][i]. Absent channels are zero.
+template <int VP, bool INTER>
+__device__ __forceinline__ void load_pairs(const uint16_t* p, const Place<VP, INTER>& at, bool on, float (&x)[2][VP]) {
+#pragma unroll
+    for (int i = 0; i < VP; ++i) x[0][i] = x[1][i] = 0.0f;
+    if constexpr (VP == 1) {
+        float f[1];
+        if (on && at.na) load_n<1>(p + at.ca, f), x[0][0] = f[0];
+        if (on && at.nb) load_n<1>(p + at.cb, f), x[1][0] = f[0];
+    } else if (on && at.na) {  // VP > 1 only where a lane's pairs are all there or all absent
+        if constexpr (INTER) {
+            float f[2 * VP];
+            load_n<2 * VP>(p + at.ca, f);
+#pragma unroll
+            for (int i = 0; i < VP; ++i) x[0][i] = f[2 * i], x[1][i] = f[2 * i + 1];
+        } else {
+            load_n<VP>(p + at.ca, x[0]);
+            load_n<VP>(p + at.cb, x[1]);
+        }
+    }
+}
+
+template <int VP, bool INTER>
+__device__ __forceinline__ void store_pairs(uint16_t* p, const Place<VP, INTER>& at, bool on, const float (&y)[2][VP]) {
+    if constexpr (VP == 1) {
+        if (on && at.na) store_n<1>(p + at.ca, y[0]);
+        if (on && at.nb) store_n<1>(p + at.cb, y[1]);
+    } else if (on && at.na) {
+        if constexpr (INTER) {
+            float f[2 * VP];
+#pragma unroll
+            for (int i = 0; i < VP; ++i) f[2 * i] = y[0][i], f[2 * i + 1] = y[1][i];
+            store_n<2 * VP>(p + at.ca, f);
+        } else {
+            store_n<VP>(p + at.ca, y[0]);
+            store_n<VP>(p + at.cb, y[1]);
+        }
+    }
+}
+
+template <int VP, bool INTER>
+__device__ __forceinline__ void load_weights(const void* w, int w_f32, const Place<VP, INTER>& at, float (&o)[2][VP]) {
+    constexpr int step = INTER ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+        const int c[2] = {at.ca + step * i, at.cb + step * i};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const bool on = i < (m ? at.nb : at.na);
+            o[m][i] = !on ? 0.0f : w_f32 ? static_cast<const float*>(w)[c[m]] : bf16_lo(static_cast<const uint16_t*>(w)[c[m]]);
+        }
+    }
+}
+
+// The sum over the G lanes of a head, in every one of them.
+__device__ __forceinline__ float head_sum(float x, int G) {
+    for (int d = 1; d < G; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+// What a wave works on: row `row` (of B*T), heads [h0, h1) of q or k.
+struct Item {
+    int64_t row;
+    int is_k, h0, h1;
+};
+
+__device__ __forceinline__ Item item_of(const NormArgs& a, int64_t i) {
+    Item t;
+    const int64_t c = i % a.chunks, qc = (a.q.heads + a.head_chunk - 1) / a.head_chunk;
+    t.row = i / a.chunks;
+    t.is_k = c >= qc;
+    const int64_t h = (t.is_k ? c - qc : c) * a.head_chunk, heads = t.is_k ? a.k.heads : a.q.heads;
+    t.h0 = static_cast<int>(h);
+    t.h1 = static_cast<int>(h + a.head_chunk < heads ? h + a.head_chunk : heads);
+    return t;
+}
+
+// True when every position lies in the table (or the status word of the check says so).
+__device__ __forceinline__ bool positions_good(const NormArgs& a) {
+    if (!a.pos) return true;
+    const int64_t n = a.B * a.T;
+    if (n > kOwnCheck) return *a.status == CCONV_OK;
+    bool bad = false;
+    for (int64_t i = threadIdx.x; i < n; i += kNormThreads) bad |= a.pos[i] < 0 || a.pos[i] >= a.P;
+    bad = __syncthreads_or(bad);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *const_cast<int32_t*>(a.status) = bad ? CCONV_ERR_INDEX : CCONV_OK;
+    return !bad;
+}
+
+template <int VP>
+__device__ __forceinline__ void load_angles(const NormArgs& a, int64_t row, int p0, float (&cs)[VP], float (&sn)[VP]) {
+    const int half = a.R / 2;
+    const int64_t pos = a.R == 0 ? 0 : a.pos ? a.pos[row] : row % a.T;
+    const float* t = a.table + pos * a.R + p0;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+        const bool on = p0 + i < half;
+        cs[i] = on ? t[i] : 1.0f;
+        sn[i] = on ? t[half + i] : 0.0f;
+    }
+}
+
+}  // namespace
+
+template <int VP, bool INTER, int SL>
+__global__ __launch_bounds__(kNormThreads) void cconv_qknorm_fwd_kernel(NormArgs a, int G) {
+    if (!positions_good(a)) return;
+    constexpr int U = VP == 4 ? 4 : 2;  // heads of a lane in flight
+    const int lane = threadIdx.x % kWave, j = lane % G, sub = lane / G, hpi = kWave / G;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kNormThreads / kWave) + wave_id();
+    if (i >= a.B * a.T * a.chunks) return;
+    const Item t = item_of(a, i);
+    const HeadRows& h = t.is_k ? a.k : a.q;
+    const int64_t b = t.row / a.T, tt = t.row % a.T;
+    const uint16_t* x = h.x + b * h.sb + tt * h.st;
+    uint16_t* y = h.y + b * h.ysb + tt * h.yst;
+    float w[SL][2][VP], cs[SL][VP], sn[SL][VP];
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+        const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+        load_weights<VP, INTER>(h.w, a.w_f32, at, w[s]);
+        load_angles<VP>(a, t.row, at.p0, cs[s], sn[s]);
+    }
+    const float inv = 1.0f / static_cast<float>(a.D);
+    for (int h0 = t.h0; h0 < t.h1; h0 += U * hpi) {
+        float v[U][SL][2][VP];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int s = 0; s < SL; ++s) {
+                const int head = h0 + u * hpi + sub;
+                const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                load_pairs<VP, INTER>(x + head * h.sh, at, head < t.h1, v[u][s]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int head = h0 + u * hpi + sub;
+            float ss = 0.0f;
+#pragma unroll
+            for (int s = 0; s < SL; ++s)
+#pragma unroll
+                for (int p = 0; p < VP; ++p) {
+                    ss = __builtin_fmaf(v[u][s][0][p], v[u][s][0][p], ss);
+                    ss = __builtin_fmaf(v[u][s][1][p], v[u][s][1][p], ss);
+                }
+            const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(head_sum(ss, G), inv, a.eps));
+#pragma unroll
+            for (int s = 0; s < SL; ++s) {
+                const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                float o[2][VP];
+#pragma unroll
+                for (int p = 0; p < VP; ++p) {
+                    const float e = v[u][s][0][p] * r * w[s][0][p], f = v[u][s][1][p] * r * w[s][1][p];
+                    const bool turn = at.p0 + p < a.R / 2;  // an unrotated channel never meets its neighbour
+                    o[0][p] = turn ? __builtin_fmaf(e, cs[s][p], -(f * sn[s][p])) : e;
+                    o[1][p] = turn ? __builtin_fmaf(f, cs[s][p], e * sn[s][p]) : f;
+                }
+                store_pairs<VP, INTER>(y + head * h.ysh, at, head < t.h1, o);
+            }
+        }
+    }
+}
+
+// dx = r (w u' - n mean(w u' n)) with n = x r, u' = dy rotated back; dw = sum u' n over all heads
+// and rows: fp32 sums of each lane, then of the wave's heads and the block's waves in a fixed
+// order, one partial per block.
+template <int VP, bool INTER, int SL>
+__global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs a, int G) {
+    if (!positions_good(a)) return;
+    constexpr int U = VP == 4 ? 2 : 1;
+    constexpr int kWaves = kNormThreads / kWave;
+    __shared__ float sums[kWaves][2][256];
+    const int lane = threadIdx.x % kWave, j = lane % G, sub = lane / G, hpi = kWave / G;
+    const int64_t items = a.B * a.T * a.chunks;
+    float dw[2][SL][2][VP];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+#pragma unroll
+            for (int p = 0; p < VP; ++p) dw[m][s][0][p] = dw[m][s][1][p] = 0.0f;
+    const float inv = 1.0f / static_cast<float>(a.D);
+
+    auto work = [&](const Item& t, const HeadRows& h, float (&acc)[SL][2][VP]) {
+        const int64_t b = t.row / a.T, tt = t.row % a.T;
+        const uint16_t* x = h.x + b * h.sb + tt * h.st;
+        const uint16_t* dy = h.dy + b * h.dsb + tt * h.dst;
+        uint16_t* dx = h.y + b * h.ysb + tt * h.yst;
+        float w[SL][2][VP], cs[SL][VP], sn[SL][VP];
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+            const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+            load_weights<VP, INTER>(h.w, a.w_f32, at, w[s]);
+            load_angles<VP>(a, t.row, at.p0, cs[s], sn[s]);
+        }
+        for (int h0 = t.h0; h0 < t.h1; h0 += U * hpi) {
+            float v[U][SL][2][VP], d[U][SL][2][VP];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int s = 0; s < SL; ++s) {
+                    const int head = h0 + u * hpi + sub;
+                    const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                    load_pairs<VP, INTER>(x + head * h.sh, at, head < t.h1, v[u][s]);
+                    load_pairs<VP, INTER>(dy + head * h.dsh, at, head < t.h1, d[u][s]);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int head = h0 + u * hpi + sub;
+                float ss = 0.0f;
+#pragma unroll
+                for (int s = 0; s < SL; ++s)
+#pragma unroll
+                    for (int p = 0; p < VP; ++p) {
+                        ss = __builtin_fmaf(v[u][s][0][p], v[u][s][0][p], ss);
+                        ss = __builtin_fmaf(v[u][s][1][p], v[u][s][1][p], ss);
+                    }
+                const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(head_sum(ss, G), inv, a.eps));
+                float along = 0.0f;
+#pragma unroll
+                for (int s = 0; s < SL; ++s) {
+                    const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+#pragma unroll
+                    for (int p = 0; p < VP; ++p) {
+                        const float e = d[u][s][0][p], f = d[u][s][1][p];
+                        const bool turn = at.p0 + p < a.R / 2;
+                        const float ue = turn ? __builtin_fmaf(e, cs[s][p], f * sn[s][p]) : e;
+                        const float uf = turn ? __builtin_fmaf(f, cs[s][p], -(e * sn[s][p])) : f;
+                        const float ne = v[u][s][0][p] * r, nf = v[u][s][1][p] * r;
+                        if (head < t.h1) {  // (absent lanes hold zeros, and r of a zero head may be infinite)
+                            acc[s][0][p] = __builtin_fmaf(ue, ne, acc[s][0][p]);
+                            acc[s][1][p] = __builtin_fmaf(uf, nf, acc[s][1][p]);
+                        }
+                        v[u][s][0][p] = ne, v[u][s][1][p] = nf;
+                        d[u][s][0][p] = ue * w[s][0][p], d[u][s][1][p] = uf * w[s][1][p];
+                        along = __builtin_fmaf(d[u][s][0][p], ne, along);
+                        along = __builtin_fmaf(d[u][s][1][p], nf, along);
+                    }
+                }
+                const float m = head_sum(along, G) * inv;
+#pragma unroll
+                for (int s = 0; s < SL; ++s) {
+                    const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                    float o[2][VP];
+#pragma unroll
+                    for (int p = 0; p < VP; ++p) {
+                        o[0][p] = r * __builtin_fmaf(-v[u][s][0][p], m, d[u][s][0][p]);
+                        o[1][p] = r * __builtin_fmaf(-v[u][s][1][p], m, d[u][s][1][p]);
+                    }
+                    store_pairs<VP, INTER>(dx + head * h.ysh, at, head < t.h1, o);
+                }
+            }
+        }
+    };
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWaves;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWaves + wave_id(); i < items; i += stride) {
+        const Item t = item_of(a, i);
+        if (t.is_k)
+            work(t, a.k, dw[1]);
+        else
+            work(t, a.q, dw[0]);
+    }
+    // the wave's lane groups, then the block's waves
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+            const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+#pragma unroll
+            for (int p = 0; p < VP; ++p)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float x = dw[m][s][q][p];
+                    for (int d = G; d < kWave; d *= 2) x += __shfl_xor(x, d);
+                    const int c = (q ? at.cb : at.ca) + (INTER ? 2 * p : p);
+                    if (sub == 0 && p < (q ? at.nb : at.na)) sums[wave_id()][m][c] = x;
+                }
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * a.D; e += kNormThreads) {
+        const int m = e / a.D, c = e % a.D;
+        float x = sums[0][m][c];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) x += sums[k][m][c];
+        a.part[static_cast<int64_t>(blockIdx.x) * 2 * a.D + e] = x;
+    }
+}
+
+// dw of q and k: a block per 16 columns, 16 threads a column.
+__global__ __launch_bounds__(256) void cconv_qknorm_dw_kernel(const float* part, int64_t blocks, int D, void* dwq,
+                                                              void* dwk, int w_f32, const int32_t* status) {
+    if (status && *status != CCONV_OK) return;
+    __shared__ float sums[16][17];
+    const int c = threadIdx.x % 16, r = threadIdx.x / 16, e = blockIdx.x * 16 + c;
+    float x = 0.0f;
+    if (e < 2 * D)
+        for (int64_t b = r; b < blocks; b += 16) x += part[b * 2 * D + e];
+    sums[r][c] = x;
+    __syncthreads();
+    if (r == 0 && e < 2 * D) {
+        for (int k = 1; k < 16; ++k) x += sums[k][c];
+        void* o = e < D ? dwq : dwk;
+        const int at = e < D ? e : e - D;
+        if (w_f32)
+            static_cast<float*>(o)[at] = x;
+        else
+            static_cast<uint16_t*>(o)[at] = static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xffffu);
+    }
+}
+
+// Many positions: one block checks them all and writes the status word.
+__global__ __launch_bounds__(1024) void cconv_qknorm_positions_kernel(const int32_t* pos, int64_t n, int64_t P,
+                                                                      int32_t* status) {
+    bool bad = false;
+    for (int64_t i = threadIdx.x; i < n; i += 4 * 1024) {
+        int32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = i + k * 1024 < n ? pos[i + k * 1024] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= v[k] < 0 || v[k] >= P;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *status = bad ? CCONV_ERR_INDEX : CCONV_OK;
+}
+
+hipError_t launch_positions(const int32_t* pos, int64_t n, int64_t P, int32_t* status, hipStream_t s) {
+    if (n <= kOwnCheck) return hipSuccess;
+    hipLaunchKernelGGL(cconv_qknorm_positions_kernel, dim3(1), dim3(1024), 0, s, pos, n, P, status);
+    return hipGetLastError();
+}
+
+static int lanes_of(int D, int R, int vec, bool inter) {
+    const int pairs = inter ? (D + 1) / 2 : R / 2 + (D - R + 1) / 2;
+    int G = 1;
+    while (G < 64 && G * vec < pairs) G *= 2;
+    return G;
+}
+
+template <bool BWD, int VP, bool INTER, int SL>
+static hipError_t norm_go(const NormArgs& a, hipStream_t s) {
+    const int G = lanes_of(a.D, a.R, VP, INTER);
+    if constexpr (BWD) {
+        hipLaunchKernelGGL((cconv_qknorm_bwd_kernel<VP, INTER, SL>), dim3(static_cast<uint32_t>(a.blocks)), dim3(kNormThreads),
+                           0, s, a, G);
+    } else {
+        const int64_t waves = a.B * a.T * a.chunks, blocks = (waves + 3) / 4;
+        hipLaunchKernelGGL((cconv_qknorm_fwd_kernel<VP, INTER, SL>), dim3(static_cast<uint32_t>(blocks)), dim3(kNormThreads), 0,
+                           s, a, G);
+    }
+    return hipGetLastError();
+}
+
+template <bool BWD>
+static hipError_t norm_pick(const NormArgs& a, int vec, bool inter, hipStream_t s) {
+    if (vec == 4) return inter ? norm_go<BWD, 4, true, 1>(a, s) : norm_go<BWD, 4, false, 1>(a, s);
+    if (vec == 2) return inter ? norm_go<BWD, 2, true, 1>(a, s) : norm_go<BWD, 2, false, 1>(a, s);
+    return inter ? norm_go<BWD, 1, true, 2>(a, s) : norm_go<BWD, 1, false, 2>(a, s);
+}
+
+hipError_t launch_qknorm_fwd(const NormArgs& a, int vec, bool inter, hipStream_t s) { return norm_pick<false>(a, vec, inter, s); }
+hipError_t launch_qknorm_bwd(const NormArgs& a, int vec, bool inter, hipStream_t s) { return norm_pick<true>(a, vec, inter, s); }
+
+hipError_t launch_qknorm_dw(const float* part, int64_t blocks, int D, void* dwq, void* dwk, int w_f32,
+                            const int32_t* status, hipStream_t s) {
+    hipLaunchKernelGGL(cconv_qknorm_dw_kernel, dim3((2 * D + 15) / 16), dim3(256), 0, s, part, blocks, D, dwq, dwk, w_f32,
+                       status);
+    return hipGetLastError();
+}
+
+}  // namespace cconv

@@ -508,6 +508,111 @@ cconv_status_t cconv_bwd_varlen_config(const void* x, int64_t x_st, const void* 
                                        void* workspace, size_t workspace_bytes, int32_t* status, int64_t D, int W,
                                        const cconv_config_t* config, cconv_stream_t stream);
 
+/*
+ * The operators of the layer around the convolution: linear attention with a decay for each
+ * head, and the norm of query and key heads with the position rotation. The conventions at the
+ * top of this file hold (caller-owned memory, work only enqueued on `stream`, capturable, fp32
+ * states, errors before anything is enqueued, a device status word for what only the device sees).
+ * Dimensions: 1 <= Dk, Dv, D <= 256; H, HV, Hq, Hk >= 1; empty batches (B, T or N zero) are CCONV_OK.
+ *
+ * cconv_rows_t: bf16 rows of heads, element (b, t, h, c) at p + b*sb + t*st + h*sh + c (elements,
+ * channels contiguous, strides >= 0, so a slice of a fused projection, a [B, H, T, D] layout or a
+ * broadcast input is one). Any alignment of 2 bytes runs; a 16-byte aligned p with strides and
+ * channels that are multiples of 8 takes 16-byte loads, a 4-byte aligned one with even strides and
+ * channels a multiple of 4 takes 8-byte ones. An output's elements must not overlap one another,
+ * and outputs must not overlap any other operand (CCONV_ERR_BAD_STRIDE, CCONV_ERR_ALIASING).
+ */
+typedef struct {
+    const void* p;
+    int64_t sb, st, sh;
+} cconv_rows_t;
+
+/*
+ * Linear attention over sequences. For value head hv, with query/key head h = hv / (HV / H) (HV a
+ * multiple of H) and decay a = exp(log_decay[hv]):
+ *     S_t = a S_{t-1} + k_t^T v_t          o_t = scale * q_t S_t
+ *   q, k        [B, T, H, Dk]; v, o [B, T, HV, Dv] (o written).
+ *   log_decay   fp32 [HV], a constant of the layer (no gradient); -inf is a decay of 0.
+ *   init_state  fp32 [B, HV, Dk, Dv], S before the first row, or NULL (zeros).
+ *   final_state fp32 [B, HV, Dk, Dv], S after the last row, or NULL.
+ *   cu_seqlens, nseq, status  packed batches as in cconv_fwd_varlen: B = 1, T rows in all, states
+ *               [nseq, HV, Dk, Dv], sb ignored; an empty sequence's final state is its init_state.
+ *               NULL cu_seqlens: fixed lengths, status is not used.
+ *   workspace   device memory of at least cconv_linattn_fwd_workspace_bytes (16-byte aligned),
+ *               overwritten; its contents need not be kept. nseq < 0 there: fixed lengths.
+ * The state is kept in fp32; q k^T (with its decays) and the state are rounded to bf16 where they
+ * are operands of a matrix product. o is rounded once more, to nearest even.
+ */
+size_t cconv_linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t nseq, int64_t HV, int64_t Dk, int64_t Dv);
+
+cconv_status_t cconv_linattn_fwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                 const float* log_decay, float scale, const float* init_state, const cconv_rows_t* o,
+                                 float* final_state, const int32_t* cu_seqlens, int64_t nseq, int32_t* status,
+                                 void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t HV,
+                                 int64_t Dk, int64_t Dv, cconv_stream_t stream);
+
+/*
+ * Its gradients, for the gradient d_o of o and d_final_state of the final state (or NULL: zeros):
+ * dq, dk [B, T, H, Dk] (summed over a group's value heads in fp32, rounded once), dv [B, T, HV, Dv],
+ * and d_init_state fp32 [B, HV, Dk, Dv] or NULL. Nothing of the forward is needed but its inputs.
+ */
+size_t cconv_linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t nseq, int64_t H, int64_t HV, int64_t Dk,
+                                         int64_t Dv);
+
+cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                 const float* log_decay, float scale, const float* init_state,
+                                 const cconv_rows_t* d_o, const float* d_final_state, const cconv_rows_t* dq,
+                                 const cconv_rows_t* dk, const cconv_rows_t* dv, float* d_init_state,
+                                 const int32_t* cu_seqlens, int64_t nseq, int32_t* status, void* workspace,
+                                 size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t HV, int64_t Dk,
+                                 int64_t Dv, cconv_stream_t stream);
+
+/*
+ * One token for each of N sequences, on a pool of states updated in place.
+ *   q, k [N, H, Dk], v, o [N, HV, Dv]: st is the stride over n, sb is ignored.
+ *   state  fp32 [S, HV, Dk, Dv] contiguous.
+ *   state_indices, status  as in cconv_update: the slot of row n, -1 for a padding row (o = 0);
+ *          indices outside [-1, S) or a slot named twice leave every state as it was and o
+ *          unspecified, with *status = CCONV_ERR_INDEX. NULL: slot n for row n (N <= S).
+ * Limits as cconv_update's: N <= 2^24; with indices, S <= 2^18.
+ */
+cconv_status_t cconv_linattn_update(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,
+                                    const float* log_decay, float scale, float* state, int64_t S,
+                                    const int32_t* state_indices, const cconv_rows_t* o, int64_t N, int64_t H,
+                                    int64_t HV, int64_t Dk, int64_t Dv, int32_t* status, cconv_stream_t stream);
+
+/*
+ * The norm of every head of q and k and the rotation by position, in one pass over both:
+ *     u = x / sqrt(mean(x^2) + eps) * w[c]      y = u with its first R channels rotated in pairs
+ *   q, yq [B, T, Hq, D]; k, yk [B, T, Hk, D]; wq, wk [D], w_dtype.
+ *   table      fp32 [P, R]: row p holds the R/2 cosines, then the R/2 sines of position p. R is even,
+ *              0 <= R <= D; NULL when R == 0.
+ *   interleaved  0: channel c < R/2 turns with c + R/2; 1: channel 2c with 2c + 1.
+ *   positions  int32 [B, T], or NULL: row t of each batch row is position t (T <= P then). Not read
+ *              when R == 0.
+ *   status     device int32, required with positions, else it may be NULL: CCONV_OK, or
+ *              CCONV_ERR_INDEX when a position lies outside [0, P) (then nothing else was written).
+ */
+cconv_status_t cconv_qknorm_fwd(const cconv_rows_t* q, const cconv_rows_t* k, const void* wq, const void* wk,
+                                cconv_dtype_t w_dtype, const float* table, int64_t P, int64_t R, int interleaved,
+                                const int32_t* positions, float eps, const cconv_rows_t* yq, const cconv_rows_t* yk,
+                                int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int32_t* status,
+                                cconv_stream_t stream);
+
+/*
+ * Its gradients: dq, dk for the gradients dyq, dyk of yq, yk, and dwq, dwk [D] in w_dtype (fp32 sums
+ * over all rows and heads in a fixed order, rounded once). workspace: at least
+ * cconv_qknorm_bwd_workspace_bytes, 16-byte aligned.
+ */
+size_t cconv_qknorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
+cconv_status_t cconv_qknorm_bwd(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* dyq,
+                                const cconv_rows_t* dyk, const void* wq, const void* wk, cconv_dtype_t w_dtype,
+                                const float* table, int64_t P, int64_t R, int interleaved, const int32_t* positions,
+                                float eps, const cconv_rows_t* dq, const cconv_rows_t* dk, void* dwq, void* dwk,
+                                void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t Hq, int64_t Hk,
+                                int64_t D, int32_t* status, cconv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
