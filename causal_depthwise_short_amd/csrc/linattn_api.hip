@@ -18,7 +18,8 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 40;    // any size times a stride stays far below 2^63
 constexpr int64_t kMaxRowCount = int64_t(1) << 31;  // rows of a packed batch (32-bit offsets)
-constexpr int64_t kMaxHeads = int64_t(1) << 16;
+constexpr int64_t kMaxWalkStride = int64_t(1) << 22;  // a chunk's 64 rows (fp32 at most) stay within 31 bits of bytes
+constexpr int64_t kMaxHeads = int64_t(1) << 14;
 constexpr int64_t kMaxHeadDim = 256;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSequences = int64_t(1) << 24;
@@ -93,6 +94,9 @@ cconv_status_t check_rows(const cconv_rows_t* r, const Dims& d, bool out) {
     return CCONV_OK;
 }
 
+// The walk addresses a chunk's rows by 32-bit offsets (a stride over one row does not matter).
+bool walkable(const cconv_rows_t& r, const Dims& d) { return d.T <= 1 || r.st <= kMaxWalkStride; }
+
 // Elements of a row that one load may take (an axis of length 1 has no stride that matters).
 int row_vec(const cconv_rows_t& r, const Dims& d) {
     const int64_t s = (d.B > 1 ? r.sb : 0) | (d.T > 1 ? r.st : 0) | (d.heads > 1 ? r.sh : 0);
@@ -102,7 +106,7 @@ int row_vec(const cconv_rows_t& r, const Dims& d) {
 }
 
 Rows rows_of(const cconv_rows_t& r, const Dims& d, int hdiv) {
-    return Rows{static_cast<const uint16_t*>(r.p), r.sb, r.st, r.sh, hdiv, static_cast<int>(d.dim), row_vec(r, d)};
+    return Rows{static_cast<const uint16_t*>(r.p), r.sb, d.T > 1 ? r.st : 0, r.sh, hdiv, static_cast<int>(d.dim), row_vec(r, d)};
 }
 
 // ---- linear attention over sequences -------------------------------------------------------
@@ -254,6 +258,7 @@ cconv_status_t cconv_linattn_fwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     if ((st = check_rows(q, dk, false)) != CCONV_OK || (st = check_rows(k, dk, false)) != CCONV_OK ||
         (st = check_rows(v, dv, false)) != CCONV_OK || (st = check_rows(o, dv, true)) != CCONV_OK)
         return st;
+    if (!walkable(*q, dk) || !walkable(*k, dk) || !walkable(*v, dv) || !walkable(*o, dv)) return CCONV_ERR_BAD_STRIDE;
     if (!aligned(init_state, 4) || !aligned(final_state, 4) || !aligned(workspace, 16)) return CCONV_ERR_MISALIGNED;
     Cut c;
     const Workspace ws = fwd_workspace(B, T, cu_seqlens ? nseq : -1, HV, Dk, Dv, &c);
@@ -285,13 +290,13 @@ cconv_status_t cconv_linattn_fwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.k = rows_of(*k, dk, grp);
     a.v = rows_of(*v, dv, 1);
     a.o = const_cast<void*>(o->p);
-    a.o_sb = o->sb, a.o_st = o->st, a.o_sh = o->sh;
+    a.o_sb = o->sb, a.o_st = T > 1 ? o->st : 0, a.o_sh = o->sh;
     a.o_vec = row_vec(*o, dv) >= 4 ? 4 : 1;
     a.log_decay = log_decay;
     a.alpha = a.beta = scale, a.gamma = 1.0f;
     a.shift = 1;
     a.init = init_state, a.fin = final_state;
-    a.sk = Dv, a.sv = 1;
+    a.sk = static_cast<int>(Dv), a.sv = 1;
     a.cu = cu_seqlens, a.status = cu_seqlens ? status : nullptr;
     a.T = T;
     a.HV = static_cast<int>(HV);
@@ -321,6 +326,8 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
         if ((st = check_rows(in[i], i < 2 ? nk : nv, false)) != CCONV_OK) return st;
     for (int i = 0; i < 3; ++i)
         if ((st = check_rows(out[i], i < 2 ? nk : nv, true)) != CCONV_OK) return st;
+    for (int i = 0; i < 4; ++i)
+        if (!walkable(*in[i], i < 2 ? nk : nv) || (i < 3 && !walkable(*out[i], i < 2 ? nk : nv))) return CCONV_ERR_BAD_STRIDE;
     if (!aligned(init_state, 4) || !aligned(d_final_state, 4) || !aligned(d_init_state, 4) || !aligned(workspace, 16))
         return CCONV_ERR_MISALIGNED;
     Cut c;
@@ -357,12 +364,12 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     auto to = [&](WalkArgs& a, const cconv_rows_t& r, const Dims& d) {
         if (d.heads == HV) {
             a.o = const_cast<void*>(r.p);
-            a.o_sb = r.sb, a.o_st = r.st, a.o_sh = r.sh;
+            a.o_sb = r.sb, a.o_st = T > 1 ? r.st : 0, a.o_sh = r.sh;
             a.o_f32 = 0;
             a.o_vec = row_vec(r, d) >= 4 ? 4 : 1;
         } else {
             a.o = p.part;
-            a.o_sh = d.dim, a.o_st = HV * d.dim, a.o_sb = T * a.o_st;
+            a.o_sh = d.dim, a.o_st = HV * d.dim, a.o_sb = T * a.o_st;  // at most 2^22, as a caller's
             a.o_f32 = 1;
             a.o_vec = d.dim % 4 == 0 ? 4 : 1;
         }
@@ -385,7 +392,7 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.alpha = a.beta = scale, a.gamma = 1.0f;
     a.shift = 1;
     a.init = init_state;
-    a.sk = 1, a.sv = Dv;
+    a.sk = 1, a.sv = static_cast<int>(Dv);
     to(a, *dq, nk);
     if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dq)) != CCONV_OK) return st;
     // dk and dv: backwards, carrying the gradient of the state
@@ -394,12 +401,12 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.alpha = scale, a.beta = 1.0f, a.gamma = scale;
     a.shift = 0, a.reverse = 1;
     a.init = d_final_state;
-    a.sk = 1, a.sv = Dv;
+    a.sk = 1, a.sv = static_cast<int>(Dv);
     to(a, *dk, nk);
     if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dk)) != CCONV_OK) return st;
     a.q = rk, a.k = rq, a.v = rdo;
     a.fin = d_init_state;
-    a.sk = Dv, a.sv = 1;
+    a.sk = static_cast<int>(Dv), a.sv = 1;
     to(a, *dv, nv);
     return walk(a, c, p, s);
 }

@@ -36,7 +36,7 @@ struct WalkArgs {
     int shift, reverse;
     const float* init;  // S before the first row of each sequence, or null (zeros)
     float* fin;         // S after the last row, or null
-    int64_t sk, sv;     // strides of init and fin over the state's two axes; a head's matrix has Dk*Dv entries
+    int sk, sv;         // strides of init and fin over the state's two axes; a head's matrix has Dk*Dv entries
     float* states;      // [segments, HV, vblocks, DK*DVB]: per segment its own sum, then (scan) its carry-in
     // packed batches: row offsets, and per segment its sequence and first row (see SegPlan)
     const int32_t* cu;

@@ -48,52 +48,65 @@ __device__ __forceinline__ float power_long(float g, int64_t n) {
                   : __builtin_amdgcn_exp2f(static_cast<float>(static_cast<double>(g) * static_cast<double>(n) * 1.4426950408889634));
 }
 
-// Eight channels of a row, of which the first `have` (<= 8, may be <= 0) exist.
-template <bool WIDE>
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, int have, int vec) {
-    u32x4 r = {0u, 0u, 0u, 0u};
-    if constexpr (WIDE) {
-        if (have > 0) r = *reinterpret_cast<const u32x4*>(p);
-    } else if (vec == 4) {
-        if (have > 0) {
-            const u32x2a v = *reinterpret_cast<const u32x2a*>(p);
-            r.x = v.x, r.y = v.y;
-        }
-        if (have > 4) {
-            const u32x2a v = *reinterpret_cast<const u32x2a*>(p + 4);
-            r.z = v.x, r.w = v.y;
-        }
+// Byte offset that lies outside every buffer range below: a load from it gives zeros, a store to it
+// is dropped.
+constexpr uint32_t kNowhere = 0x80000000u;
+constexpr int kRange = 0x7fffffff;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, kRange, 0x00020000);
+}
+
+// Eight channels of a row, of which the first `have` exist (VEC = 8: all or, at kNowhere, none). No
+// branches, so a chunk's loads are issued back to back and stay in flight.
+template <int VEC>
+__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff, int have) {
+    if constexpr (VEC == 8) {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+    } else if constexpr (VEC == 4) {
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, soff, 0));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, have > 4 ? off + 8 : kNowhere, soff, 0));
+        return u32x4{x.x, x.y, y.x, y.y};
     } else {
         uint32_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = i < have ? p[i] : 0u;
-        r.x = e[0] | e[1] << 16, r.y = e[2] | e[3] << 16, r.z = e[4] | e[5] << 16, r.w = e[6] | e[7] << 16;
+        for (int i = 0; i < 8; ++i)
+            e[i] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, i < have ? off + 2 * i : kNowhere, soff, 0));
+        return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
-    return r;
 }
 
 // One operand's part in the staging of a chunk: 256 threads, eight channels each, COLS (padded)
-// channels a row.
-template <int COLS, bool WIDE>
+// channels a row. The chunk is addressed from its lowest row in memory: its first row, or, walked
+// backwards, its 64th (which may lie before the sequence: rows past the end are never read).
+template <int COLS, int VEC>
 struct Stage {
     static constexpr int kPerRow = COLS / 8, kRows = 256 / kPerRow, kPasses = kChunk / kRows, kPitch = COLS + 8;
     u32x4 r[kPasses];
-    const uint16_t* p;  // the thread's place in the chunk's first pass
-    int64_t step;       // elements of one row
-    int row, have, vec;
+    const uint16_t* p;  // lowest row of the next chunk
+    int64_t step;       // elements from a chunk to the next
+    int pass;           // bytes between a thread's rows of two passes (first row to last of the chunk, upwards)
+    int row, have;      // the thread's row in pass 0 and its channels
+    uint32_t off;
+    bool up;
 
-    __device__ __forceinline__ void open(const uint16_t* base, int64_t st, int col0, int dim, int v) {
+    __device__ __forceinline__ void open(const uint16_t* first_row, const Rows& x, bool reverse, int col0) {
         row = threadIdx.x / kPerRow;
-        const int col = (threadIdx.x % kPerRow) * 8;
-        have = dim - col0 - col;
-        step = st;
-        vec = v;
-        p = base + row * st + col0 + col;
+        const int col = col0 + (threadIdx.x % kPerRow) * 8;
+        have = x.dim - col;
+        up = !reverse;
+        p = reverse ? first_row - (kChunk - 1) * x.st : first_row;
+        step = reverse ? -kChunk * x.st : kChunk * x.st;
+        const int st = static_cast<int>(x.st);
+        pass = kRows * st * 2;
+        off = have <= 0 ? kNowhere : static_cast<uint32_t>(((reverse ? kRows - 1 - row : row) * st + col) * 2);
     }
     __device__ __forceinline__ void load(int n) {
+        const __amdgpu_buffer_rsrc_t b = chunk_rsrc(p);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) r[i] = load8<WIDE>(p + i * kRows * step, row + i * kRows < n ? have : 0, vec);
-        p += kChunk * step;
+        for (int i = 0; i < kPasses; ++i)
+            r[i] = load8<VEC>(b, row + i * kRows < n ? off : kNowhere, (up ? i : kPasses - 1 - i) * pass, have);
+        p += step;
     }
     __device__ __forceinline__ void store(uint16_t* lds) {
         uint16_t* d = lds + row * kPitch + (threadIdx.x % kPerRow) * 8;
@@ -106,7 +119,7 @@ __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) <= 3
 
 }  // namespace
 
-template <int DK, int NV, bool WIDE, bool STATES>
+template <int DK, int NV, int VEC, bool STATES>
 __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16, NK = DK / 32;
     constexpr int PK = DK + 8, PV = DVB + 8, PP = kChunk + 8;
@@ -116,10 +129,10 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
     __shared__ __align__(16) uint16_t lp[STATES ? 8 : kChunk * PP];
 
     if (a.status && *a.status != CCONV_OK) return;
-    const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
-    const int vb = static_cast<int>(tile % a.vblocks);
-    const int hv = static_cast<int>(tile / a.vblocks % a.HV);
-    const int64_t seg = tile / (static_cast<int64_t>(a.vblocks) * a.HV);
+    const uint32_t tile = static_cast<uint32_t>(xcd_tile(blockIdx.x, gridDim.x)), per_seg = static_cast<uint32_t>(a.vblocks * a.HV);
+    const uint32_t hvb = tile % per_seg;
+    const int vb = static_cast<int>(hvb % a.vblocks), hv = static_cast<int>(hvb / a.vblocks);
+    const int64_t seg = tile / per_seg;
     int64_t seq, start, len, first;  // the segment's sequence, its rows, and the segment's first row in it
     if (a.cu) {
         seq = a.seg_of[2 * seg];
@@ -128,8 +141,8 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         start = a.cu[seq];
         len = a.cu[seq + 1] - start;
     } else {
-        seq = seg / a.segs;
-        first = seg % a.segs * a.seg_rows;
+        seq = static_cast<uint32_t>(seg) / static_cast<uint32_t>(a.segs);
+        first = (seg - seq * a.segs) * a.seg_rows;
         start = 0;
         len = a.T;
     }
@@ -144,14 +157,13 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 
     // rows are taken in the walk's order: backwards from the last row when reversed
     const int64_t row0 = start + (a.reverse ? len - 1 - first : first);
-    const int64_t dir = a.reverse ? -1 : 1;
     auto base = [&](const Rows& x) { return x.p + batch * x.sb + row0 * x.st + (hv / x.hdiv) * x.sh; };
-    Stage<DK, WIDE> sk;
-    Stage<DVB, WIDE> sv;
-    Stage<STATES ? 64 : DK, WIDE> sq;
-    sk.open(base(a.k), dir * a.k.st, 0, a.k.dim, a.k.vec);
-    sv.open(base(a.v), dir * a.v.st, vb * DVB, a.v.dim, a.v.vec);
-    if constexpr (!STATES) sq.open(base(a.q), dir * a.q.st, 0, a.q.dim, a.q.vec);
+    Stage<DK, VEC> sk;
+    Stage<DVB, VEC> sv;
+    Stage<STATES ? 64 : DK, VEC> sq;
+    sk.open(base(a.k), a.k, a.reverse, 0);
+    sv.open(base(a.v), a.v, a.reverse, vb * DVB);
+    if constexpr (!STATES) sq.open(base(a.q), a.q, a.reverse, 0);
 
     int n = static_cast<int>(rows < kChunk ? rows : kChunk);
     sk.load(n);
@@ -178,6 +190,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         }
         if (a.init) {
             const float w = power_long(a.log_decay[hv], first);
+            const __amdgpu_buffer_rsrc_t ib = chunk_rsrc(a.init + matrix);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -185,8 +198,8 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int dk = 16 * t + 4 * g + r, dv = dv0 + 16 * m + i16;
-                        if (dk < a.k.dim && dv < a.v.dim)
-                            S[t][m][r] = __builtin_fmaf(w, a.init[matrix + dk * a.sk + dv * a.sv], S[t][m][r]);
+                        const uint32_t at = dk < a.k.dim && dv < a.v.dim ? 4 * (dk * a.sk + dv * a.sv) : kNowhere;
+                        S[t][m][r] = __builtin_fmaf(w, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ib, at, 0, 0)), S[t][m][r]);
                     }
         }
     }
@@ -210,11 +223,11 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
     const float early = power(g2, 32);
 
     for (int64_t c0 = 0; c0 < rows; c0 += kChunk) {
-        __syncthreads();  // the chunk before has been read
+        lds_barrier();  // the chunk before has been read
         sk.store(lk);
         sv.store(lv);
         if constexpr (!STATES) sq.store(lq);
-        __syncthreads();
+        lds_barrier();
         const int left = static_cast<int>(rows - c0 < 2 * kChunk ? rows - c0 : 2 * kChunk);
         n = left < kChunk ? left : kChunk;
         if (left > kChunk) {
@@ -264,41 +277,41 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
             // o^T = S^T q^T: the state rounded to bf16 as a matrix operand (a relative 2^-9 of each
             // entry, as the products' other operand has; the state itself stays in 32 bits)
             f32x4 O[4][NM];
-            auto from_state = [&]() {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
-                    for (int m = 0; m < NM; ++m) O[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int m = 0; m < NM; ++m) O[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) {
-                    u32x4 sf[NM];
+            for (int kk = 0; kk < NK; ++kk) {
+                u32x4 sf[NM];
 #pragma unroll
-                    for (int m = 0; m < NM; ++m) {
-                        const f32x4 x = S[2 * kk][m], y = S[2 * kk + 1][m];
-                        sf[m] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
-                                      pack_bf16x2(y[2], y[3])};
-                    }
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint16_t* p = lq + (16 * b + i16) * PK + 32 * kk + 4 * g;
-                        const u32x2 lo = *reinterpret_cast<const u32x2*>(p), hi = *reinterpret_cast<const u32x2*>(p + 16);
-                        const u32x4 qt = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-                        for (int m = 0; m < NM; ++m) O[b][m] = mfma(sf[m], qt, O[b][m]);
-                    }
+                for (int m = 0; m < NM; ++m) {
+                    const f32x4 x = S[2 * kk][m], y = S[2 * kk + 1][m];
+                    sf[m] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                                  pack_bf16x2(y[2], y[3])};
                 }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < 4; ++b) {
+                    const uint16_t* p = lq + (16 * b + i16) * PK + 32 * kk + 4 * g;
+                    const u32x2 lo = *reinterpret_cast<const u32x2*>(p), hi = *reinterpret_cast<const u32x2*>(p + 16);
+                    const u32x4 qt = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-                    for (int m = 0; m < NM; ++m)
+                    for (int m = 0; m < NM; ++m) O[b][m] = mfma(sf[m], qt, O[b][m]);
+                }
+            }
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) O[b][m][r] *= carry[b];
-            };
-            from_state();
-            __syncthreads();  // p is whole
-            float sum = 0.0f;
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[b][m][r] *= carry[b];
+            lds_barrier();  // p is whole
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
+                f32x4 enter[NM];
+                float sum = 0.0f;
+#pragma unroll
+                for (int m = 0; m < NM; ++m) enter[m] = O[b][m];
 #pragma unroll
                 for (int h = 0; h <= b / 2; ++h) {
                     const u32x4 pf = *reinterpret_cast<const u32x4*>(lp + (16 * b + i16) * PP + 32 * h + 8 * g);
@@ -309,13 +322,12 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(O[b][m][r], 0.0f, sum);
-            }
-            // An infinity or NaN in a later row of v meets p's zeros above the diagonal and would
-            // make NaN of rows that do not depend on it: such a chunk is summed again without them.
-            if (__builtin_amdgcn_ballot_w64(sum != 0.0f)) {
-                from_state();
+                // An infinity or NaN in a later row of v meets p's zeros above the diagonal and would make
+                // NaN of rows that do not depend on it: such rows are summed again without them.
+                if (__builtin_expect(__builtin_amdgcn_ballot_w64(sum != 0.0f) != 0, 0)) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                    for (int m = 0; m < NM; ++m) O[b][m] = enter[m];
+#pragma clang loop unroll(disable)
                     for (int j = 0; j <= 16 * b + i16; ++j) {
                         const float pj = bf16_lo(lp[(16 * b + i16) * PP + j]);
 #pragma unroll
@@ -324,38 +336,36 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
                             for (int r = 0; r < 4; ++r)
                                 O[b][m][r] = __builtin_fmaf(pj, bf16_lo(lv[j * PV + wave * NV + 16 * m + 4 * g + r]), O[b][m][r]);
                     }
+                }
             }
+            // rows of o, addressed like the operands' from the chunk's lowest row
+            const int es = a.o_f32 ? 4 : 2, ost = static_cast<int>(a.o_st) * es;
+            const int64_t low = row0 + (a.reverse ? -(c0 + kChunk - 1) : c0);
+            const __amdgpu_buffer_rsrc_t ob =
+                chunk_rsrc(static_cast<char*>(a.o) + (batch * a.o_sb + low * a.o_st + hv * a.o_sh) * es);
+            const uint32_t o0 = static_cast<uint32_t>((a.reverse ? 15 - i16 : i16) * ost + (dv0 + 4 * g) * es);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const int r0 = 16 * b + i16;
-                if (r0 >= n) continue;
-                const int64_t at = batch * a.o_sb + (row0 + dir * (c0 + r0)) * a.o_st + hv * a.o_sh;
+                const int sb = (a.reverse ? 3 - b : b) * 16 * ost;
+                const bool in = 16 * b + i16 < n;
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
                     const int dv = dv0 + 16 * m + 4 * g;
-                    if (dv >= a.v.dim) continue;
-                    if (a.o_f32) {
-                        float* o = static_cast<float*>(a.o) + at + dv;
-                        if (a.o_vec == 4) {
-                            *reinterpret_cast<f32x4*>(o) = O[b][m];
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (dv + r < a.v.dim) o[r] = O[b][m][r];
-                        }
+                    const uint32_t at = in && dv < a.v.dim ? o0 + 16 * m * es : kNowhere;
+                    const u32x2 w = {pack_bf16x2(O[b][m][0], O[b][m][1]), pack_bf16x2(O[b][m][2], O[b][m][3])};
+                    if (a.o_vec == 4) {
+                        if (a.o_f32)
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[b][m]), ob, at, sb, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b64(w, ob, at, sb, 0);
                     } else {
-                        uint16_t* o = static_cast<uint16_t*>(a.o) + at + dv;
-                        const u32x2 w = {pack_bf16x2(O[b][m][0], O[b][m][1]), pack_bf16x2(O[b][m][2], O[b][m][3])};
-                        if (a.o_vec == 4) {
-                            u32x2a wa;
-                            wa.x = w.x, wa.y = w.y;
-                            *reinterpret_cast<u32x2a*>(o) = wa;
-                        } else {
-                            const uint16_t e[4] = {static_cast<uint16_t>(w.x), static_cast<uint16_t>(w.x >> 16),
-                                                   static_cast<uint16_t>(w.y), static_cast<uint16_t>(w.y >> 16)};
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (dv + r < a.v.dim) o[r] = e[r];
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t e = dv + r < a.v.dim ? at + r * es : kNowhere;
+                            if (a.o_f32)
+                                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[b][m][r]), ob, e, sb, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w[r / 2] >> (16 * (r % 2))), ob, e, sb, 0);
                         }
                     }
                 }
@@ -418,6 +428,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 #pragma unroll
             for (int m = 0; m < NM; ++m) *reinterpret_cast<f32x4*>(c + (t * NM + m) * 1024) = S[t][m];
     } else if (last && a.fin) {
+        const __amdgpu_buffer_rsrc_t fb = chunk_rsrc(a.fin + matrix);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -425,7 +436,8 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int dk = 16 * t + 4 * g + r, dv = dv0 + 16 * m + i16;
-                    if (dk < a.k.dim && dv < a.v.dim) a.fin[matrix + dk * a.sk + dv * a.sv] = S[t][m][r];
+                    const uint32_t at = dk < a.k.dim && dv < a.v.dim ? 4 * (dk * a.sk + dv * a.sv) : kNowhere;
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][m][r]), fb, at, 0, 0);
                 }
     }
 }
@@ -528,29 +540,28 @@ WalkShape walk_shape(int64_t Dk, int64_t Dv) {
     return w;
 }
 
-template <int DK, int NV>
-static hipError_t walk_go(bool wide, bool states, const WalkArgs& a, hipStream_t s) {
+template <int DK, int NV, int VEC>
+static hipError_t walk_go(bool states, const WalkArgs& a, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(a.segments * a.HV * a.vblocks)), block(256);
-    if (states) {
-        if (wide)
-            hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, true, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, false, true>), grid, block, 0, s, a);
-    } else {
-        if (wide)
-            hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, true, false>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, false, false>), grid, block, 0, s, a);
-    }
+    if (states)
+        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
+template <int DK, int NV>
+static hipError_t walk_vec(int vec, bool states, const WalkArgs& a, hipStream_t s) {
+    if (vec == 8) return walk_go<DK, NV, 8>(states, a, s);
+    return vec == 4 ? walk_go<DK, NV, 4>(states, a, s) : walk_go<DK, NV, 1>(states, a, s);
+}
+
 hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, hipStream_t s) {
-    const bool wide = a.k.vec == 8 && a.v.vec == 8 && (states_only || a.q.vec == 8);
-    if (w.DK == 64) return w.NV == 32 ? walk_go<64, 32>(wide, states_only, a, s) : walk_go<64, 16>(wide, states_only, a, s);
-    if (w.DK == 128)
-        return w.NV == 32 ? walk_go<128, 32>(wide, states_only, a, s) : walk_go<128, 16>(wide, states_only, a, s);
-    return walk_go<256, 16>(wide, states_only, a, s);
+    int vec = a.k.vec < a.v.vec ? a.k.vec : a.v.vec;
+    if (!states_only && a.q.vec < vec) vec = a.q.vec;
+    if (w.DK == 64) return w.NV == 32 ? walk_vec<64, 32>(vec, states_only, a, s) : walk_vec<64, 16>(vec, states_only, a, s);
+    if (w.DK == 128) return w.NV == 32 ? walk_vec<128, 32>(vec, states_only, a, s) : walk_vec<128, 16>(vec, states_only, a, s);
+    return walk_vec<256, 16>(vec, states_only, a, s);
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {

@@ -513,7 +513,7 @@ cconv_status_t cconv_bwd_varlen_config(const void* x, int64_t x_st, const void* 
  * head, and the norm of query and key heads with the position rotation. The conventions at the
  * top of this file hold (caller-owned memory, work only enqueued on `stream`, capturable, fp32
  * states, errors before anything is enqueued, a device status word for what only the device sees).
- * Dimensions: 1 <= Dk, Dv, D <= 256; H, HV, Hq, Hk >= 1; empty batches (B, T or N zero) are CCONV_OK.
+ * Dimensions: 1 <= Dk, Dv, D <= 256; 1 <= H, HV, Hq, Hk <= 2^14; empty batches (B, T or N zero) are CCONV_OK.
  *
  * cconv_rows_t: bf16 rows of heads, element (b, t, h, c) at p + b*sb + t*st + h*sh + c (elements,
  * channels contiguous, strides >= 0, so a slice of a fused projection, a [B, H, T, D] layout or a
@@ -538,6 +538,8 @@ typedef struct {
  *   cu_seqlens, nseq, status  packed batches as in cconv_fwd_varlen: B = 1, T rows in all, states
  *               [nseq, HV, Dk, Dv], sb ignored; an empty sequence's final state is its init_state.
  *               NULL cu_seqlens: fixed lengths, status is not used.
+ *   Row strides (st) are at most 2^22 elements here and in cconv_linattn_bwd (CCONV_ERR_BAD_STRIDE): a
+ *               chunk's rows are addressed by 32-bit byte offsets.
  *   workspace   device memory of at least cconv_linattn_fwd_workspace_bytes (16-byte aligned),
  *               overwritten; its contents need not be kept. nseq < 0 there: fixed lengths.
  * The state is kept in fp32; q k^T (with its decays) and the state are rounded to bf16 where they
