@@ -76,12 +76,28 @@ __device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, i
     }
 }
 
-// One operand's part in the staging of a chunk: 256 threads, eight channels each, COLS (padded)
+// LDS tiles have rows of COLS bf16 channels without padding; the 16-byte chunk c of row r lies at place
+// c ^ swizzle(r) of its row. The order is chosen for both ways a tile is read: 16-byte reads of 16 rows
+// at one chunk (fragments of rows; lanes 0-3, 12-15 and 20-27 go together), and transposing 8-byte reads
+// of two chunks of eight rows (half a wave). Both then touch every one of the 64 banks once. (Padded rows
+// had two-way conflicts in either, 17% of the walk's cycles.)
+template <int COLS>
+__device__ __forceinline__ int swizzle(int row) {
+    if constexpr (COLS == 64) {
+        const int v = (row >> 1) & 7;
+        return (((v & 3) ^ ((v & 4) >> 1)) << 1) | (v >> 2);
+    } else {
+        const int r = row & 15;
+        return (((r & 7) ^ ((r & 8) >> 1)) << 1) | (r >> 3);
+    }
+}
+
+// One operand's part in the staging of a chunk: THREADS threads, eight channels each, COLS (padded)
 // channels a row. The chunk is addressed from its lowest row in memory: its first row, or, walked
 // backwards, its 64th (which may lie before the sequence: rows past the end are never read).
-template <int COLS, int VEC>
+template <int COLS, int VEC, int THREADS>
 struct Stage {
-    static constexpr int kPerRow = COLS / 8, kRows = 256 / kPerRow, kPasses = kChunk / kRows, kPitch = COLS + 8;
+    static constexpr int kPerRow = COLS / 8, kRows = THREADS / kPerRow, kPasses = kChunk / kRows;
     u32x4 r[kPasses];
     const uint16_t* p;  // lowest row of the next chunk
     int64_t step;       // elements from a chunk to the next
@@ -109,337 +125,507 @@ struct Stage {
         p += step;
     }
     __device__ __forceinline__ void store(uint16_t* lds) {
-        uint16_t* d = lds + row * kPitch + (threadIdx.x % kPerRow) * 8;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) *reinterpret_cast<u32x4*>(d + i * kRows * kPitch) = r[i];
+        for (int i = 0; i < kPasses; ++i) {
+            const int r0 = kRows % 16 == 0 ? row : row + i * kRows;  // (a multiple of 16 rows leaves the place as it is)
+            *reinterpret_cast<u32x4*>(lds + (row + i * kRows) * COLS + ((threadIdx.x % kPerRow) ^ swizzle<COLS>(r0)) * 8) = r[i];
+        }
     }
 };
 
-__device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) <= 3.402823466e38f; }
+constexpr int kPitchP = kChunk + 8;  // p's rows in LDS
 
-}  // namespace
-
-template <int DK, int NV, int VEC, bool STATES>
-__global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
-    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16, NK = DK / 32;
-    constexpr int PK = DK + 8, PV = DVB + 8, PP = kChunk + 8;
-    __shared__ __align__(16) uint16_t lk[kChunk * PK];
-    __shared__ __align__(16) uint16_t lv[kChunk * PV];
-    __shared__ __align__(16) uint16_t lq[STATES ? 8 : kChunk * PK];
-    __shared__ __align__(16) uint16_t lp[STATES ? 8 : kChunk * PP];
-
-    if (a.status && *a.status != CCONV_OK) return;
-    const uint32_t tile = static_cast<uint32_t>(xcd_tile(blockIdx.x, gridDim.x)), per_seg = static_cast<uint32_t>(a.vblocks * a.HV);
-    const uint32_t hvb = tile % per_seg;
-    const int vb = static_cast<int>(hvb % a.vblocks), hv = static_cast<int>(hvb / a.vblocks);
-    const int64_t seg = tile / per_seg;
-    int64_t seq, start, len, first;  // the segment's sequence, its rows, and the segment's first row in it
-    if (a.cu) {
-        seq = a.seg_of[2 * seg];
-        if (seq < 0) return;
-        first = static_cast<int64_t>(a.seg_of[2 * seg + 1]) * a.seg_rows;
-        start = a.cu[seq];
-        len = a.cu[seq + 1] - start;
-    } else {
-        seq = static_cast<uint32_t>(seg) / static_cast<uint32_t>(a.segs);
-        first = (seg - seq * a.segs) * a.seg_rows;
-        start = 0;
-        len = a.T;
+// Powers of the decay in LDS, the same for every chunk (held in registers, they made the walk spill).
+struct Table {
+    alignas(16) float score[kChunk];   // alpha * a^n: scores of rows n apart
+    alignas(16) float carry[kChunk];   // beta * a^(r + shift): what the state gives row r
+    alignas(16) float weight[kChunk];  // gamma * a^(64 - shift - r): row r of a full chunk in the state
+    __device__ __forceinline__ void fill(float g2, float alpha, float beta, float gamma, int shift, int i) {
+        if (i >= kChunk) return;
+        score[i] = alpha * power(g2, i);
+        carry[i] = beta * power(g2, i + shift);
+        weight[i] = gamma * power(g2, kChunk - shift - i);
     }
-    const bool last = first + a.seg_rows >= len;
-    if (STATES && last) return;
-    const int64_t rows = last ? len - first : a.seg_rows;
-    const int64_t batch = a.cu ? 0 : seq;
+};
 
-    const int wave = wave_id(), lane = threadIdx.x % kWave, i16 = lane % 16, g = lane / 16;
-    const float g2 = a.log_decay[hv] * 1.4426950408889634f;
-    const float aC = power(g2, kChunk);
+// One wave's part in a walk: a state of DK keys by NV value channels, and the products of a chunk.
+// The 32 rows of a product over rows are taken in the order 4g + 0..3, 16 + 4g + 0..3 by lane group g,
+// as the transposing loads give them without conflicts; keys are taken in the same order in o = q S,
+// where the state's tiles hold them so.
+template <int DK, int NV, int COLSV>
+struct Wave {
+    static constexpr int NM = NV / 16, NT = DK / 16, NK = DK / 32;
+    f32x4 S[NT][NM];  // S[t][m]: keys 16t + 4g + 0..3 of value channel 16m + i16
+    u32x4 vf[2][NM];  // value channel 16m + i16 of rows 32h + 4g + 0..3 and 32h + 16 + 4g + 0..3
+    float g2, aC, gamma;
+    int i16, g, shift;
 
-    // rows are taken in the walk's order: backwards from the last row when reversed
-    const int64_t row0 = start + (a.reverse ? len - 1 - first : first);
-    auto base = [&](const Rows& x) { return x.p + batch * x.sb + row0 * x.st + (hv / x.hdiv) * x.sh; };
-    Stage<DK, VEC> sk;
-    Stage<DVB, VEC> sv;
-    Stage<STATES ? 64 : DK, VEC> sq;
-    sk.open(base(a.k), a.k, a.reverse, 0);
-    sv.open(base(a.v), a.v, a.reverse, vb * DVB);
-    if constexpr (!STATES) sq.open(base(a.q), a.q, a.reverse, 0);
-
-    int n = static_cast<int>(rows < kChunk ? rows : kChunk);
-    sk.load(n);
-    sv.load(n);
-    if constexpr (!STATES) sq.load(n);
-
-    // the state: S[t][m] holds keys 16t + 4g + 0..3 of value channel dv0 + 16m + i16
-    const int dv0 = vb * DVB + wave * NV;
-    f32x4 S[NT][NM];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < NM; ++m) S[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int64_t frag = (static_cast<int64_t>(hv) * a.vblocks + vb) * DK * DVB + (wave * 64 + lane) * 4;
-    const int64_t seg_floats = static_cast<int64_t>(a.HV) * a.vblocks * DK * DVB;
-    const int64_t matrix = (seq * a.HV + hv) * static_cast<int64_t>(a.k.dim) * a.v.dim;
-    if constexpr (!STATES) {
-        if (first > 0) {
-            const float* c = a.states + (seg - 1) * seg_floats + frag;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int m = 0; m < NM; ++m) S[t][m] = *reinterpret_cast<const f32x4*>(c + (t * NM + m) * 1024);
-        }
-        if (a.init) {
-            const float w = power_long(a.log_decay[hv], first);
-            const __amdgpu_buffer_rsrc_t ib = chunk_rsrc(a.init + matrix);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int dk = 16 * t + 4 * g + r, dv = dv0 + 16 * m + i16;
-                        const uint32_t at = dk < a.k.dim && dv < a.v.dim ? 4 * (dk * a.sk + dv * a.sv) : kNowhere;
-                        S[t][m][r] = __builtin_fmaf(w, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ib, at, 0, 0)), S[t][m][r]);
-                    }
-        }
-    }
-
-    // decays that stay the same from chunk to chunk
-    float near[4], far[4], carry[4];  // p's diagonal tile; p's tiles below, less 16 rows a tile; rows 16b + i16
-    if constexpr (!STATES) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = i16 - 4 * g - r;
-            near[r] = a.alpha * power(g2, d < 0 ? 0 : d);
-            far[r] = a.alpha * power(g2, 16 + d);
-            carry[r] = a.beta * power(g2, 16 * r + i16 + a.shift);
-        }
-        // p's tiles above the diagonal are read by the 32-row products and stay zero
-        for (int i = threadIdx.x; i < kChunk * PP / 2; i += 256) reinterpret_cast<uint32_t*>(lp)[i] = 0u;
-    }
-    float late[8];  // row 8g + e of a full chunk's second half
-#pragma unroll
-    for (int e = 0; e < 8; ++e) late[e] = a.gamma * power(g2, 32 - a.shift - 8 * g - e);
-    const float early = power(g2, 32);
-
-    for (int64_t c0 = 0; c0 < rows; c0 += kChunk) {
-        lds_barrier();  // the chunk before has been read
-        sk.store(lk);
-        sv.store(lv);
-        if constexpr (!STATES) sq.store(lq);
-        lds_barrier();
-        const int left = static_cast<int>(rows - c0 < 2 * kChunk ? rows - c0 : 2 * kChunk);
-        n = left < kChunk ? left : kChunk;
-        if (left > kChunk) {
-            sk.load(left - kChunk);
-            sv.load(left - kChunk);
-            if constexpr (!STATES) sq.load(left - kChunk);
-        }
-        u32x4 vf[2][NM];  // value channel dv0 + 16m + i16, rows 32h + 8g + 0..7
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const uint16_t* p = lv + (32 * h + 8 * g + i16 / 4) * PV + wave * NV + 16 * m + 4 * (i16 % 4);
-                const u32x2 lo = load_tr(p), hi = load_tr(p + 4 * PV);
-                vf[h][m] = u32x4{lo.x, lo.y, hi.x, hi.y};
-            }
-
-        if constexpr (!STATES) {
-            // p^T = k q^T, rows 16*wave + i16 of q
-            u32x4 qf[NK];
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
-                qf[kk] = *reinterpret_cast<const u32x4*>(lq + (16 * wave + i16) * PK + 32 * kk + 8 * g);
-            float down = 1.0f;  // a^(16 * (tiles between))
-            const float a16 = power(g2, 16);
-#pragma unroll
-            for (int back = 0; back < 4; ++back) {
-                const int jb = wave - back;
-                if (jb >= 0) {
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int kk = 0; kk < NK; ++kk)
-                        acc = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * PK + 32 * kk + 8 * g), qf[kk], acc);
-                    float p[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (back == 0)  // a later row's product is dropped, whatever it holds
-                            p[r] = i16 >= 4 * g + r ? acc[r] * near[r] : 0.0f;
-                        else
-                            p[r] = acc[r] * (far[r] * down);
-                    }
-                    if (back > 0) down *= a16;
-                    *reinterpret_cast<u32x2*>(lp + (16 * wave + i16) * PP + 16 * jb + 4 * g) =
-                        u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
-                }
-            }
-            // o^T = S^T q^T: the state rounded to bf16 as a matrix operand (a relative 2^-9 of each
-            // entry, as the products' other operand has; the state itself stays in 32 bits)
-            f32x4 O[4][NM];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int m = 0; m < NM; ++m) O[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) {
-                u32x4 sf[NM];
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    const f32x4 x = S[2 * kk][m], y = S[2 * kk + 1][m];
-                    sf[m] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
-                                  pack_bf16x2(y[2], y[3])};
-                }
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint16_t* p = lq + (16 * b + i16) * PK + 32 * kk + 4 * g;
-                    const u32x2 lo = *reinterpret_cast<const u32x2*>(p), hi = *reinterpret_cast<const u32x2*>(p + 16);
-                    const u32x4 qt = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) O[b][m] = mfma(sf[m], qt, O[b][m]);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) O[b][m][r] *= carry[b];
-            lds_barrier();  // p is whole
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                f32x4 enter[NM];
-                float sum = 0.0f;
-#pragma unroll
-                for (int m = 0; m < NM; ++m) enter[m] = O[b][m];
-#pragma unroll
-                for (int h = 0; h <= b / 2; ++h) {
-                    const u32x4 pf = *reinterpret_cast<const u32x4*>(lp + (16 * b + i16) * PP + 32 * h + 8 * g);
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) O[b][m] = mfma(vf[h][m], pf, O[b][m]);
-                }
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(O[b][m][r], 0.0f, sum);
-                // An infinity or NaN in a later row of v meets p's zeros above the diagonal and would make
-                // NaN of rows that do not depend on it: such rows are summed again without them.
-                if (__builtin_expect(__builtin_amdgcn_ballot_w64(sum != 0.0f) != 0, 0)) {
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) O[b][m] = enter[m];
-#pragma clang loop unroll(disable)
-                    for (int j = 0; j <= 16 * b + i16; ++j) {
-                        const float pj = bf16_lo(lp[(16 * b + i16) * PP + j]);
-#pragma unroll
-                        for (int m = 0; m < NM; ++m)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                O[b][m][r] = __builtin_fmaf(pj, bf16_lo(lv[j * PV + wave * NV + 16 * m + 4 * g + r]), O[b][m][r]);
-                    }
-                }
-            }
-            // rows of o, addressed like the operands' from the chunk's lowest row
-            const int es = a.o_f32 ? 4 : 2, ost = static_cast<int>(a.o_st) * es;
-            const int64_t low = row0 + (a.reverse ? -(c0 + kChunk - 1) : c0);
-            const __amdgpu_buffer_rsrc_t ob =
-                chunk_rsrc(static_cast<char*>(a.o) + (batch * a.o_sb + low * a.o_st + hv * a.o_sh) * es);
-            const uint32_t o0 = static_cast<uint32_t>((a.reverse ? 15 - i16 : i16) * ost + (dv0 + 4 * g) * es);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int sb = (a.reverse ? 3 - b : b) * 16 * ost;
-                const bool in = 16 * b + i16 < n;
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    const int dv = dv0 + 16 * m + 4 * g;
-                    const uint32_t at = in && dv < a.v.dim ? o0 + 16 * m * es : kNowhere;
-                    const u32x2 w = {pack_bf16x2(O[b][m][0], O[b][m][1]), pack_bf16x2(O[b][m][2], O[b][m][3])};
-                    if (a.o_vec == 4) {
-                        if (a.o_f32)
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[b][m]), ob, at, sb, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b64(w, ob, at, sb, 0);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const uint32_t e = dv + r < a.v.dim ? at + r * es : kNowhere;
-                            if (a.o_f32)
-                                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[b][m][r]), ob, e, sb, 0);
-                            else
-                                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w[r / 2] >> (16 * (r % 2))), ob, e, sb, 0);
-                        }
-                    }
-                }
-            }
-        }
-
-        // S = a^n S + k^T (a^(n-shift-j) v): the weighted v as a sum of two bf16 values (the second
-        // holds what the first rounds off), so the state keeps about 17 bits of every term
-        const float an = n == kChunk ? aC : power(g2, n);
+    __device__ __forceinline__ void open(float log_decay, float gamma_, int shift_) {
+        i16 = threadIdx.x % 16, g = threadIdx.x % kWave / 16;
+        g2 = log_decay * 1.4426950408889634f;
+        gamma = gamma_, shift = shift_;
+        aC = power(g2, kChunk);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
+            for (int m = 0; m < NM; ++m) S[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // row of element e of a transposed fragment, within its 32 rows
+    __device__ __forceinline__ int row_of(int e) const { return 4 * g + (e & 3) + 16 * (e >> 2); }
+
+    // channels 16x + i16 of rows 32h + .. of a tile of COLS channels
+    template <int COLS>
+    __device__ __forceinline__ u32x4 columns(const uint16_t* tile, int x, int h) const {
+        const int row = 4 * g + i16 / 4;
+        const uint16_t* p = tile + row * COLS + (((2 * x + (i16 % 4) / 2) ^ swizzle<COLS>(row)) * 8 + 4 * (i16 % 2)) + 32 * h * COLS;
+        const u32x2 lo = load_tr(p), hi = load_tr(p + 16 * COLS);
+        return u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
+    __device__ __forceinline__ void load_values(const uint16_t* lv, int col0) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[t][m][r] *= an;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV>(lv, col0 / 16 + m, h);
+    }
+
+    // S = S * keep + k^T (weight * v), where row j of the chunk (n rows) has weight gamma * a^(n-shift-j) *
+    // more. The weighted v is taken as a sum of two bf16 values (the second holds what the first rounds
+    // off), so the state keeps about 17 bits of every term.
+    template <bool KEEP>
+    __device__ __forceinline__ void update(const uint16_t* lk, const Table& tab, int n, float more) {
+        if constexpr (KEEP) {
+            const float an = n == kChunk ? aC : power(g2, n);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[t][m][r] *= an;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 4 * g),
+                           *reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 16 + 4 * g)};
             float w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = h == 0 ? late[e] * early : late[e];
+            for (int e = 0; e < 8; ++e) w[e] = KEEP ? wt[e / 4][e % 4] : wt[e / 4][e % 4] * more;
             if (n < kChunk) {  // rows past the end hold zeros; their weight only has to be finite
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int left_rows = n - a.shift - 32 * h - 8 * g - e;
-                    w[e] = a.gamma * power(g2, left_rows < 0 ? 0 : left_rows);
+                    const int left = n - shift - 32 * h - row_of(e);
+                    w[e] = gamma * power(g2, left < 0 ? 0 : left) * more;
                 }
             }
             u32x4 hi[NM], lo[NM];
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                uint32_t x[4], y[4];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const float u0 = bf16_lo(vf[h][m][d]) * w[2 * d], u1 = bf16_hi(vf[h][m][d]) * w[2 * d + 1];
-                    x[d] = pack_bf16x2(u0, u1);
-                    const float l0 = u0 - bf16_lo(x[d]), l1 = u1 - bf16_hi(x[d]);
-                    y[d] = pack_bf16x2(finite(l0) ? l0 : 0.0f, finite(l1) ? l1 : 0.0f);
+                    const uint32_t x = pack_bf16x2(u0, u1);
+                    hi[m][d] = x;
+                    // of an infinite or NaN value the rest is made finite: the first part carries it
+                    lo[m][d] = pack_bf16x2(__builtin_amdgcn_fmed3f(u0 - bf16_lo(x), -1e38f, 1e38f),
+                                           __builtin_amdgcn_fmed3f(u1 - bf16_hi(x), -1e38f, 1e38f));
                 }
-                hi[m] = u32x4{x[0], x[1], x[2], x[3]};
-                lo[m] = u32x4{y[0], y[1], y[2], y[3]};
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const uint16_t* p = lk + (32 * h + 8 * g + i16 / 4) * PK + 16 * t + 4 * (i16 % 4);
-                const u32x2 k0 = load_tr(p), k1 = load_tr(p + 4 * PK);
-                const u32x4 kf = {k0.x, k0.y, k1.x, k1.y};
+                const u32x4 kf = columns<DK>(lk, t, h);
+#pragma unroll
+                for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf, lo[m], S[t][m]);
+#pragma unroll
+                for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf, hi[m], S[t][m]);
+            }
+        }
+    }
+};
+
+// The same value, unknown to the compiler: what is computed from it is computed in place. (LDS addresses
+// kept from chunk to chunk cost the walk registers that it had to spill.)
+__device__ __forceinline__ int anew(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// p^T = k q^T with its decays, rows 16w + i16 of q, to LDS.
+template <int DK>
+__device__ __forceinline__ void scores(const uint16_t* lq, const uint16_t* lk, uint16_t* lp, int w, const Table& tab, int i16,
+                                       int g) {
+    constexpr int NK = DK / 32;
+    i16 = anew(i16);
+    const int sw = swizzle<DK>(i16);
+    u32x4 qf[NK];
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk)
+        qf[kk] = *reinterpret_cast<const u32x4*>(lq + (16 * w + i16) * DK + ((4 * kk + g) ^ sw) * 8);
+#pragma unroll
+    for (int back = 0; back < 4; ++back) {
+        const int jb = w - back;
+        if (jb >= 0) {
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+                acc = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * DK + ((4 * kk + g) ^ sw) * 8), qf[kk], acc);
+            float p[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int apart = 16 * back + i16 - 4 * g - r;
+                p[r] = acc[r] * tab.score[back == 0 && apart < 0 ? 0 : apart];
+                if (back == 0 && apart < 0) p[r] = 0.0f;  // a later row's product is dropped, whatever it holds
+            }
+            *reinterpret_cast<u32x2*>(lp + (16 * w + i16) * kPitchP + 16 * jb + 4 * g) =
+                u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+        }
+    }
+}
+
+// o^T = S^T q^T: O[b][m] holds value channels 16m + 4g + 0..3 of row 16b + i16. The state is rounded to
+// bf16 as a matrix operand (a relative 2^-9 of each entry, as the products' other operand has; the
+// state itself stays in 32 bits).
+template <int DK, int NV, int COLSV>
+__device__ __forceinline__ void from_state(const Wave<DK, NV, COLSV>& w, const uint16_t* lq, const Table& tab,
+                                           f32x4 (&O)[4][NV / 16]) {
+    constexpr int NM = NV / 16, NK = DK / 32;
+    const int sw = swizzle<DK>(w.i16);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int m = 0; m < NM; ++m) O[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+        u32x4 sf[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const f32x4 x = w.S[2 * kk][m], y = w.S[2 * kk + 1][m];
+            sf[m] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        }
+        const uint16_t* row = lq + w.i16 * DK + 4 * (w.g % 2);
+        const int c = 4 * kk + w.g / 2;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + (c ^ sw) * 8 + 16 * b * DK);
+            const u32x2 hi = *reinterpret_cast<const u32x2*>(row + ((c + 2) ^ sw) * 8 + 16 * b * DK);
+            const u32x4 qt = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+            for (int m = 0; m < NM; ++m) O[b][m] = mfma(sf[m], qt, O[b][m]);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float carry = tab.carry[16 * b + w.i16];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[b][m][r] *= carry;
+    }
+}
+
+// O += v^T p^T.
+template <int DK, int NV, int COLSV>
+__device__ __forceinline__ void from_rows(const Wave<DK, NV, COLSV>& w, const uint16_t* lp, const uint16_t* lv, int col0,
+                                          f32x4 (&O)[4][NV / 16]) {
+    constexpr int NM = NV / 16;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        f32x4 enter[NM];
+        float sum = 0.0f;
+        const uint16_t* row = lp + (16 * b + w.i16) * kPitchP;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) enter[m] = O[b][m];
+#pragma unroll
+        for (int h = 0; h <= b / 2; ++h) {
+            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 32 * h + 4 * w.g);
+            const u32x2 hi = *reinterpret_cast<const u32x2*>(row + 32 * h + 16 + 4 * w.g);
+            const u32x4 pf = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+            for (int m = 0; m < NM; ++m) O[b][m] = mfma(w.vf[h][m], pf, O[b][m]);
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(O[b][m][r], 0.0f, sum);
+        // An infinity or NaN in a later row of v meets p's zeros above the diagonal and would make NaN of
+        // rows that do not depend on it: such rows are summed again without them.
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(sum != 0.0f) != 0, 0)) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) O[b][m] = enter[m];
+#pragma clang loop unroll(disable)
+            for (int j = 0; j <= 16 * b + w.i16; ++j) {
+                const float pj = bf16_lo(row[j]);
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    S[t][m] = mfma(kf, lo[m], S[t][m]);
-                    S[t][m] = mfma(kf, hi[m], S[t][m]);
+                    const int c = col0 + 16 * m + 4 * w.g;
+                    const uint16_t* v = lv + j * COLSV + ((c / 8) ^ swizzle<COLSV>(j)) * 8 + c % 8;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[b][m][r] = __builtin_fmaf(pj, bf16_lo(v[r]), O[b][m][r]);
                 }
             }
         }
     }
+}
 
-    if constexpr (STATES) {
-        float* c = a.states + seg * seg_floats + frag;
+// Where a wave's rows of o go, addressed like the operands' from each chunk's lowest row. bf16 rows whose
+// channels go out four at a time are kept packed and stored one chunk late, before the next chunk's
+// loads are issued: stores count with the loads that a wave waits for, and a store waited for right after
+// its issue held up every chunk.
+template <int NV>
+struct Output {
+    static constexpr int NM = NV / 16;
+    char* p;  // the row before the walk's first chunk's lowest
+    int64_t step;
+    u32x2 held[4][NM];
+    int held_rows;
+    uint32_t off[NM];
+    int st16, es, vec, dim, dv, i16;
+    bool f32, up;
+
+    __device__ __forceinline__ void open(void* o, int64_t head_off, int64_t row0, int64_t o_st, int o_f32, int o_vec, bool reverse,
+                                         int dim_, int dv_, int i16_, int g) {
+        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, dim = dim_, dv = dv_ + 4 * g, i16 = i16_, up = !reverse;
+        p = static_cast<char*>(o) + (head_off + (reverse ? row0 - (kChunk - 1) : row0) * o_st) * es;
+        step = (reverse ? -kChunk : kChunk) * o_st * es;
+        const int st = static_cast<int>(o_st) * es;
+        st16 = 16 * st;
+        held_rows = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < NM; ++m)
+            off[m] = dv + 16 * m < dim ? static_cast<uint32_t>((reverse ? 15 - i16 : i16) * st + (dv + 16 * m) * es) : kNowhere;
+    }
+    __device__ __forceinline__ void flush() {
+        if (held_rows == 0) return;
+        const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
+        p += step;
 #pragma unroll
-            for (int m = 0; m < NM; ++m) *reinterpret_cast<f32x4*>(c + (t * NM + m) * 1024) = S[t][m];
-    } else if (last && a.fin) {
-        const __amdgpu_buffer_rsrc_t fb = chunk_rsrc(a.fin + matrix);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int m = 0; m < NM; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int dk = 16 * t + 4 * g + r, dv = dv0 + 16 * m + i16;
-                    const uint32_t at = dk < a.k.dim && dv < a.v.dim ? 4 * (dk * a.sk + dv * a.sv) : kNowhere;
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][m][r]), fb, at, 0, 0);
-                }
+                __builtin_amdgcn_raw_buffer_store_b64(held[b][m], ob, 16 * b + i16 < held_rows ? off[m] : kNowhere,
+                                                      (up ? b : 3 - b) * st16, 0);
+        held_rows = 0;
     }
+    __device__ __forceinline__ void put(const f32x4 (&O)[4][NM], int n) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                held[b][m] = u32x2{pack_bf16x2(O[b][m][0], O[b][m][1]), pack_bf16x2(O[b][m][2], O[b][m][3])};
+        held_rows = n;
+        if (vec == 4 && !f32) return;
+        held_rows = 0;
+        const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
+        p += step;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int sb = (up ? b : 3 - b) * st16;
+            const bool in = 16 * b + i16 < n;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const uint32_t at = in ? off[m] : kNowhere;
+                if (vec == 4) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[b][m]), ob, at, sb, 0);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t e = dv + 16 * m + r < dim ? at + r * es : kNowhere;
+                        if (f32)
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[b][m][r]), ob, e, sb, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(held[b][m][r / 2] >> (16 * (r % 2))), ob,
+                                                                  e, sb, 0);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// The segment a workgroup works on. False: nothing to do.
+struct Segment {
+    int64_t seq, seg, start, len, first, rows;
+    int hv, vb;
+    bool last;
+    __device__ __forceinline__ bool open(const WalkArgs& a) {
+        const uint32_t tile = static_cast<uint32_t>(xcd_tile(blockIdx.x, gridDim.x));
+        const uint32_t per_seg = static_cast<uint32_t>(a.vblocks * a.HV), hvb = tile % per_seg;
+        vb = static_cast<int>(hvb % a.vblocks), hv = static_cast<int>(hvb / a.vblocks);
+        seg = tile / per_seg;
+        if (a.cu) {
+            seq = a.seg_of[2 * seg];
+            if (seq < 0) return false;
+            first = static_cast<int64_t>(a.seg_of[2 * seg + 1]) * a.seg_rows;
+            start = a.cu[seq];
+            len = a.cu[seq + 1] - start;
+        } else {
+            seq = static_cast<uint32_t>(seg) / static_cast<uint32_t>(a.segs);
+            first = (seg - seq * a.segs) * a.seg_rows;
+            start = 0;
+            len = a.T;
+        }
+        last = first + a.seg_rows >= len;
+        rows = last ? len - first : a.seg_rows;
+        return true;
+    }
+    __device__ __forceinline__ int64_t batch(const WalkArgs& a) const { return a.cu ? 0 : seq; }
+    // the first row in the walk's order: backwards from the last row when reversed
+    __device__ __forceinline__ int64_t row0(bool reverse) const { return start + (reverse ? len - 1 - first : first); }
+    __device__ __forceinline__ const uint16_t* row(const WalkArgs& a, const Rows& x, int64_t r) const {
+        return x.p + batch(a) * x.sb + r * x.st + (hv / x.hdiv) * x.sh;
+    }
+};
+
+// Entries (dk, dv) of a head's matrix: a wave's state from it (added, weighted) and to it.
+template <int DK, int NV, int COLSV>
+__device__ __forceinline__ void add_matrix(Wave<DK, NV, COLSV>& w, const float* m0, float weight, int Dk, int Dv, int dv0, int sk,
+                                           int sv) {
+    const __amdgpu_buffer_rsrc_t b = chunk_rsrc(m0);
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int m = 0; m < NV / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int dk = 16 * t + 4 * w.g + r, dv = dv0 + 16 * m + w.i16;
+                const uint32_t at = dk < Dk && dv < Dv ? 4 * (dk * sk + dv * sv) : kNowhere;
+                w.S[t][m][r] = __builtin_fmaf(weight, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0)), w.S[t][m][r]);
+            }
+}
+
+template <int DK, int NV, int COLSV>
+__device__ __forceinline__ void store_matrix(const Wave<DK, NV, COLSV>& w, float* m0, int Dk, int Dv, int dv0, int sk, int sv) {
+    const __amdgpu_buffer_rsrc_t b = chunk_rsrc(m0);
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int m = 0; m < NV / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int dk = 16 * t + 4 * w.g + r, dv = dv0 + 16 * m + w.i16;
+                const uint32_t at = dk < Dk && dv < Dv ? 4 * (dk * sk + dv * sv) : kNowhere;
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(w.S[t][m][r]), b, at, 0, 0);
+            }
+}
+
+}  // namespace
+
+// The walk. Four waves, NV value channels each.
+template <int DK, int NV, int VEC>
+__global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
+    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
+    __shared__ __align__(16) uint16_t lq[kChunk * DK];
+    __shared__ __align__(16) uint16_t lk[kChunk * DK];
+    __shared__ __align__(16) uint16_t lv[kChunk * DVB];
+    __shared__ __align__(16) uint16_t lp[kChunk * kPitchP];
+    __shared__ Table tab;
+
+    if (a.status && *a.status != CCONV_OK) return;
+    Segment s;
+    if (!s.open(a)) return;
+    const int64_t row0 = s.row0(a.reverse);
+    Stage<DK, VEC, 256> sq, sk;
+    Stage<DVB, VEC, 256> sv;
+    sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+    sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
+    sq.open(s.row(a, a.q, row0), a.q, a.reverse, 0);
+    int n = static_cast<int>(s.rows < kChunk ? s.rows : kChunk);
+    sk.load(n);
+    sv.load(n);
+    sq.load(n);
+
+    const int wave = wave_id(), lane = threadIdx.x % kWave;
+    Wave<DK, NV, DVB> w;
+    w.open(a.log_decay[s.hv], a.gamma, a.shift);
+    tab.fill(w.g2, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
+    const int dv0 = s.vb * DVB + wave * NV;
+    const int64_t matrix = (s.seq * a.HV + s.hv) * static_cast<int64_t>(a.k.dim) * a.v.dim;
+    if (s.first > 0) {
+        const float* c = a.states + ((s.seg - 1) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB +
+                         s.vb * DK * DVB + (wave * 64 + lane) * 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) w.S[t][m] = *reinterpret_cast<const f32x4*>(c + (t * NM + m) * 1024);
+    }
+    if (a.init)
+        add_matrix(w, a.init + matrix, power_long(a.log_decay[s.hv], s.first), a.k.dim, a.v.dim, dv0, a.sk, a.sv);
+    Output<NV> out;
+    out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, dv0, w.i16, w.g);
+    // p's tiles above the diagonal are read by the 32-row products and stay zero
+    for (int i = threadIdx.x; i < kChunk * kPitchP / 2; i += 256) reinterpret_cast<uint32_t*>(lp)[i] = 0u;
+
+    const int rows = static_cast<int>(s.rows);
+    for (int c0 = 0; c0 < rows; c0 += kChunk) {
+        lds_barrier();  // the chunk before has been read
+        sk.store(lk);
+        sv.store(lv);
+        sq.store(lq);
+        lds_barrier();
+        out.flush();
+        n = rows - c0 < kChunk ? rows - c0 : kChunk;
+        if (rows - c0 > kChunk) {
+            sk.load(rows - c0 - kChunk);
+            sv.load(rows - c0 - kChunk);
+            sq.load(rows - c0 - kChunk);
+        }
+        scores<DK>(lq, lk, lp, wave, tab, w.i16, w.g);
+        f32x4 O[4][NM];
+        from_state(w, lq, tab, O);
+        w.load_values(lv, wave * NV);
+        lds_barrier();  // p is whole
+        from_rows(w, lp, lv, wave * NV, O);
+        out.put(O, n);
+        w.template update<true>(lk, tab, n, 1.0f);
+    }
+    out.flush();
+    if (s.last && a.fin) store_matrix(w, a.fin + matrix, a.k.dim, a.v.dim, dv0, a.sk, a.sv);
+}
+
+// Each segment's own sum of k^T v, for the segments that another follows. The chunks are taken from the
+// segment's last to its first: their weights then only grow smaller, so the state needs no scaling, and
+// the rows read last are those that the walk after it reads first.
+template <int DK, int NV, int VEC>
+__global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a) {
+    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
+    __shared__ __align__(16) uint16_t lk[kChunk * DK];
+    __shared__ __align__(16) uint16_t lv[kChunk * DVB];
+    __shared__ Table tab;
+
+    if (a.status && *a.status != CCONV_OK) return;
+    Segment s;
+    if (!s.open(a) || s.last) return;  // (so the segment is whole)
+    const int rows = static_cast<int>(s.rows);
+    const int64_t row0 = s.row0(a.reverse) + (a.reverse ? -(rows - kChunk) : rows - kChunk);
+    Stage<DK, VEC, 256> sk;
+    Stage<DVB, VEC, 256> sv;
+    sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+    sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
+    sk.step = -sk.step, sv.step = -sv.step;
+    sk.load(kChunk);
+    sv.load(kChunk);
+    const int wave = wave_id(), lane = threadIdx.x % kWave;
+    Wave<DK, NV, DVB> w;
+    w.open(a.log_decay[s.hv], a.gamma, a.shift);
+    tab.fill(w.g2, 0.0f, 0.0f, a.gamma, a.shift, threadIdx.x);
+    float more = 1.0f;
+    for (int c0 = 0; c0 < rows; c0 += kChunk) {
+        lds_barrier();
+        sk.store(lk);
+        sv.store(lv);
+        lds_barrier();
+        if (rows - c0 > kChunk) {
+            sk.load(kChunk);
+            sv.load(kChunk);
+        }
+        w.load_values(lv, wave * NV);
+        w.template update<false>(lk, tab, kChunk, more);
+        more *= w.aC;
+    }
+    float* c = a.states + (s.seg * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
+               (wave * 64 + lane) * 4;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int m = 0; m < NM; ++m) *reinterpret_cast<f32x4*>(c + (t * NM + m) * 1024) = w.S[t][m];
 }
 
 // One workgroup per (sequence, head, 1024 floats): the running sum over the sequence's segments.
@@ -457,11 +643,19 @@ __global__ __launch_bounds__(256) void cconv_linattn_scan_kernel(ScanArgs a) {
     f32x4* p = reinterpret_cast<f32x4*>(a.states + (s0 * a.HV + hv) * a.floats + part * 1024) + threadIdx.x;
     const int64_t step = a.HV * a.floats / 4;
     f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t s = s0; s + 1 < s1; ++s, p += step) {
-        const f32x4 x = *p;
+    constexpr int kAhead = 8;  // loads in flight
+    for (int64_t s = s0; s + 1 < s1; s += kAhead, p += kAhead * step) {
+        f32x4 x[kAhead];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(w, c[r], x[r]);
-        *p = c;
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i + 1 < s1) x[i] = p[i * step];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s + i + 1 >= s1) break;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(w, c[r], x[i][r]);
+            p[i * step] = c;
+        }
     }
 }
 
@@ -544,9 +738,9 @@ template <int DK, int NV, int VEC>
 static hipError_t walk_go(bool states, const WalkArgs& a, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(a.segments * a.HV * a.vblocks)), block(256);
     if (states)
-        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
