@@ -27,7 +27,7 @@ constexpr int64_t kMaxDecodeRows = int64_t(1) << 24;
 constexpr int64_t kMaxStepSlots = int64_t(1) << 18;  // the slot check's bits next to the step's own LDS
 // Segments: enough workgroups for two on each of the 256 CUs, each of at least kMinSegment rows (a
 // segment costs one more read of its k and v and two passes over its state).
-constexpr int64_t kTargetGroups = 512;
+constexpr int64_t kTargetGroups = 256;
 constexpr int64_t kMinSegment = 256;
 constexpr int64_t kNormWaves = 4096;      // waves a norm wants before a wave takes several heads in turn
 constexpr int64_t kNormBwdBlocks = 1024;  // blocks of the norm's backward, each with one partial of dw
@@ -113,6 +113,7 @@ Rows rows_of(const cconv_rows_t& r, const Dims& d, int hdiv) {
 
 struct Cut {
     int64_t nseq, seg_rows, segs, segments;
+    int sub;  // parts in which a segment's own sum is taken
 };
 
 int64_t value_blocks(const WalkShape& w, int64_t Dv) { return (Dv + 4 * w.NV - 1) / (4 * w.NV); }
@@ -123,7 +124,8 @@ Cut cut_of(int64_t B, int64_t T, int64_t nseq, int64_t groups) {
     const int64_t rows = B * T;
     const int64_t want = std::max<int64_t>(1, kTargetGroups / std::max<int64_t>(1, groups));  // segments in all
     const int64_t each = std::max<int64_t>(kMinSegment, (rows + want - 1) / want);
-    c.seg_rows = (each + kChunk - 1) / kChunk * kChunk;
+    c.sub = each >= 2 * kMinSegment ? 2 : 1;
+    c.seg_rows = (each + c.sub * kChunk - 1) / (c.sub * kChunk) * (c.sub * kChunk);
     if (nseq < 0) {
         c.nseq = B;
         c.segs = std::max<int64_t>(1, (T + c.seg_rows - 1) / c.seg_rows);
@@ -161,7 +163,7 @@ Workspace fwd_workspace(int64_t B, int64_t T, int64_t nseq, int64_t HV, int64_t 
     const WalkShape w = walk_shape(Dk, Dv);
     *cut = cut_of(B, T, nseq, HV * value_blocks(w, Dv));
     Workspace ws;
-    if (cut->segs > 1) ws.states = align16(cut->segments * HV * state_floats(w, Dv) * 4);
+    if (cut->segs > 1) ws.states = align16(cut->segments * cut->sub * HV * state_floats(w, Dv) * 4);
     ws.plan = plan_bytes(*cut, nseq);
     return ws;
 }
@@ -170,7 +172,7 @@ Workspace bwd_workspace(int64_t B, int64_t T, int64_t nseq, int64_t H, int64_t H
     const WalkShape kv = walk_shape(Dk, Dv), vk = walk_shape(Dv, Dk);
     *cut = cut_of(B, T, nseq, HV * std::min(value_blocks(kv, Dv), value_blocks(vk, Dk)));
     Workspace ws;
-    if (cut->segs > 1) ws.states = align16(cut->segments * HV * std::max(state_floats(kv, Dv), state_floats(vk, Dk)) * 4);
+    if (cut->segs > 1) ws.states = align16(cut->segments * cut->sub * HV * std::max(state_floats(kv, Dv), state_floats(vk, Dk)) * 4);
     ws.plan = plan_bytes(*cut, nseq);
     if (HV > H) ws.part = align16(B * T * HV * Dk * 4);
     return ws;
@@ -199,11 +201,12 @@ Prepared carve(void* workspace, const Workspace& ws, const Cut& c) {
     return r;
 }
 
-cconv_status_t walk(const WalkArgs& args, const Cut& c, const Prepared& p, hipStream_t s) {
+cconv_status_t walk(const WalkArgs& args, const Cut& c, const Prepared& p, hipStream_t s, const SecondWalk* second = nullptr) {
     WalkArgs a = args;
     const WalkShape w = walk_shape(a.k.dim, a.v.dim);
     a.vblocks = static_cast<int>(value_blocks(w, a.v.dim));
     a.states = p.states;
+    a.sub = c.sub;
     a.seg_of = a.cu ? p.seg_of : nullptr;
     a.seg_rows = c.seg_rows;
     a.segs = c.segs;
@@ -220,9 +223,11 @@ cconv_status_t walk(const WalkArgs& args, const Cut& c, const Prepared& p, hipSt
         sc.nseq = c.nseq;
         sc.floats = state_floats(w, a.v.dim);
         sc.HV = a.HV;
+        sc.sub = c.sub;
         if (launch_scan(sc, s) != hipSuccess) return CCONV_ERR_LAUNCH;
     }
-    return launch_walk(w, false, a, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
+    const hipError_t e = second ? launch_walk2(w, a, *second, s) : launch_walk(w, false, a, s);
+    return e == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
 }
 
 // What the forward and the backward check alike. `n`: state rows.
@@ -395,7 +400,14 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.sk = 1, a.sv = static_cast<int>(Dv);
     to(a, *dq, nk);
     if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dq)) != CCONV_OK) return st;
-    // dk and dv: backwards, carrying the gradient of the state
+    // dk and dv: backwards, carrying the gradient of the state; together where one workgroup holds all of it
+    WalkArgs d = base;
+    d.q = rk, d.k = rq, d.v = rdo;
+    d.alpha = scale, d.beta = 1.0f, d.gamma = scale;
+    d.shift = 0, d.reverse = 1;
+    d.init = d_final_state, d.fin = d_init_state;
+    d.sk = static_cast<int>(Dv), d.sv = 1;
+    to(d, *dv, nv);
     a = base;
     a.q = rv, a.k = rdo, a.v = rq;
     a.alpha = scale, a.beta = 1.0f, a.gamma = scale;
@@ -403,12 +415,13 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.init = d_final_state;
     a.sk = 1, a.sv = static_cast<int>(Dv);
     to(a, *dk, nk);
+    if (Dk <= 128 && Dv <= 128) {
+        const SecondWalk z{a.q, a.o, a.o_sb, a.o_st, a.o_sh, a.o_f32, a.o_vec};
+        if ((st = walk(d, c, p, s, &z)) != CCONV_OK) return st;
+        return sum(*dk);
+    }
     if ((st = walk(a, c, p, s)) != CCONV_OK || (st = sum(*dk)) != CCONV_OK) return st;
-    a.q = rk, a.k = rq, a.v = rdo;
-    a.fin = d_init_state;
-    a.sk = static_cast<int>(Dv), a.sv = 1;
-    to(a, *dv, nv);
-    return walk(a, c, p, s);
+    return walk(d, c, p, s);
 }
 
 cconv_status_t cconv_linattn_update(const cconv_rows_t* q, const cconv_rows_t* k, const cconv_rows_t* v,

@@ -37,7 +37,10 @@ struct WalkArgs {
     const float* init;  // S before the first row of each sequence, or null (zeros)
     float* fin;         // S after the last row, or null
     int sk, sv;         // strides of init and fin over the state's two axes; a head's matrix has Dk*Dv entries
-    float* states;      // [segments, HV, vblocks, DK*DVB]: per segment its own sum, then (scan) its carry-in
+    // [segments, sub, HV, vblocks, DK*DVB]: the sums of a segment's `sub` parts, then (scan), in the first
+    // part's place, what enters the segment after it
+    float* states;
+    int sub;
     // packed batches: row offsets, and per segment its sequence and first row (see SegPlan)
     const int32_t* cu;
     const int32_t* seg_of;
@@ -55,9 +58,20 @@ struct WalkShape {
 };
 WalkShape walk_shape(int64_t Dk, int64_t Dv);
 
+// The walk that goes with another one whose state is the transpose of its own: rows q, values the other's
+// keys and keys the other's values.
+struct SecondWalk {
+    Rows q;
+    void* o;
+    int64_t o_sb, o_st, o_sh;
+    int o_f32, o_vec;
+};
+// For Dk, Dv <= 128 (one block of value channels).
+hipError_t launch_walk2(const WalkShape& w, const WalkArgs& a, const SecondWalk& z, hipStream_t s);
+
 hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, hipStream_t s);
 
-// Carry-in of every segment after a sequence's first: states[seg] becomes the sum that enters
+// Carry-in of every segment after a sequence's first: states[seg, 0] becomes the sum that enters
 // segment seg + 1. `seq_seg` (packed): first segment of each sequence, nseq + 1 entries.
 struct ScanArgs {
     float* states;
@@ -65,7 +79,7 @@ struct ScanArgs {
     const int32_t* seq_seg;
     const int32_t* status;
     int64_t seg_rows, segs, nseq, floats;  // floats: per (segment, head), all value blocks
-    int HV;
+    int HV, sub;
 };
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 

@@ -8,14 +8,18 @@
 // registers. The gradients are the same walk with other operands (dq: the rows do, v, k; and
 // backwards in time dk: v, do, q; dv: k, q, do).
 //
-// A workgroup of four waves walks one segment of a sequence for one value head and one block of
-// value channels; a wave owns NV of them, with all DK key channels of their state. Every product
-// is laid out so that what one leaves in registers is what the next takes:
-//   * the state as S[m = key][n = value channel] (a lane holds one value channel, four
-//     consecutive keys a tile) is the left operand of o^T = S^T q^T, and
-//   * v read from LDS by the transposing loads (a lane holds one value channel, eight
-//     consecutive rows) serves o^T = v^T p^T from the left and S = k^T v from the right.
-// Only p = (q k^T with its decays) goes through LDS, wave w computing rows 16w .. 16w + 15.
+// A workgroup walks one segment of a sequence for one value head and one block of value channels, with
+// two kinds of waves that work side by side on the same chunk:
+//   * four state waves hold the state in fp32, each all DK keys of NV value channels. In chunk c they
+//     make the state that enters chunk c + 1 and leave a bf16 copy of it in LDS;
+//   * four row waves make the outputs, 16 rows each: scores against the chunk's earlier rows, products
+//     with the state's copy, products with v.
+// k, v and the copy of the state are double-buffered, so a chunk costs one barrier, and its time is the
+// longer of the two waves' parts, not their sum (with every wave doing both parts in turn, three barriers
+// a chunk, a chunk took 4.5 us; see the figures at the kernels).
+// Every product is laid out so that what one leaves in registers is what the next takes: scores as
+// p^T[m = row j][n = row i] are the right operand of o^T = v^T p^T, with v read from LDS by the transposing
+// loads; rows of q go from memory straight to fragments.
 #include "../../include/cconv.h"
 #include "cconv_device.hpp"
 #include "linattn_internal.hpp"
@@ -76,6 +80,11 @@ __device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, i
     }
 }
 
+// `sum`, or NaN where one of the two bf16 values is infinite or NaN.
+__device__ __forceinline__ float nan_if_special(uint32_t pair, float sum) {
+    return __builtin_fmaf(bf16_lo(pair), 0.0f, __builtin_fmaf(bf16_hi(pair), 0.0f, sum));
+}
+
 // LDS tiles have rows of COLS bf16 channels without padding; the 16-byte chunk c of row r lies at place
 // c ^ swizzle(r) of its row. The order is chosen for both ways a tile is read: 16-byte reads of 16 rows
 // at one chunk (fragments of rows; lanes 0-3, 12-15 and 20-27 go together), and transposing 8-byte reads
@@ -124,6 +133,15 @@ struct Stage {
             r[i] = load8<VEC>(b, row + i * kRows < n ? off : kNowhere, (up ? i : kPasses - 1 - i) * pass, have);
         p += step;
     }
+    // Whether the wave's part of the staged chunk holds an infinity or NaN.
+    __device__ __forceinline__ bool special() const {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) sum = nan_if_special(r[i][d], sum);
+        return __builtin_amdgcn_ballot_w64(sum != 0.0f) != 0;
+    }
     __device__ __forceinline__ void store(uint16_t* lds) {
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
@@ -133,7 +151,35 @@ struct Stage {
     }
 };
 
-constexpr int kPitchP = kChunk + 8;  // p's rows in LDS
+// Channels 16x + i16 of rows row0 + 4g + 0..3 of a tile (row0 a multiple of 16).
+template <int COLS>
+__device__ __forceinline__ u32x2 half_columns(const uint16_t* tile, int x, int row0, int i16, int g) {
+    const int row = 4 * g + i16 / 4;
+    return load_tr(tile + (row0 + row) * COLS + ((2 * x + (i16 % 4) / 2) ^ swizzle<COLS>(row)) * 8 + 4 * (i16 % 2));
+}
+
+// Channels 16x + i16 of 32 rows from 32h on, as a lane's eight elements of a product over rows: rows
+// 8g + 0..7 (NATURAL), or 4g + 0..3 and 16 + 4g + 0..3, the order in which a wave holds scores.
+template <int COLS, bool NATURAL>
+__device__ __forceinline__ u32x4 columns(const uint16_t* tile, int x, int h, int i16, int g) {
+    u32x2 lo, hi;
+    if constexpr (NATURAL) {
+        const int ra = 8 * g + i16 / 4, rb = ra + 4, c = 2 * x + (i16 % 4) / 2;
+        lo = load_tr(tile + (32 * h + ra) * COLS + (c ^ swizzle<COLS>(ra)) * 8 + 4 * (i16 % 2));
+        hi = load_tr(tile + (32 * h + rb) * COLS + (c ^ swizzle<COLS>(rb)) * 8 + 4 * (i16 % 2));
+    } else {
+        lo = half_columns<COLS>(tile, x, 32 * h, i16, g);
+        hi = half_columns<COLS>(tile, x, 32 * h + 16, i16, g);
+    }
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// The same value, unknown to the compiler: what is computed from it is computed in place. (LDS addresses
+// kept from chunk to chunk cost the walks registers that they had to spill.)
+__device__ __forceinline__ int anew(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // Powers of the decay in LDS, the same for every chunk (held in registers, they made the walk spill).
 struct Table {
@@ -148,13 +194,10 @@ struct Table {
     }
 };
 
-// One wave's part in a walk: a state of DK keys by NV value channels, and the products of a chunk.
-// The 32 rows of a product over rows are taken in the order 4g + 0..3, 16 + 4g + 0..3 by lane group g,
-// as the transposing loads give them without conflicts; keys are taken in the same order in o = q S,
-// where the state's tiles hold them so.
+// A state wave: a state of DK keys by NV value channels in fp32, and its update by a chunk.
 template <int DK, int NV, int COLSV>
 struct Wave {
-    static constexpr int NM = NV / 16, NT = DK / 16, NK = DK / 32;
+    static constexpr int NM = NV / 16, NT = DK / 16;
     f32x4 S[NT][NM];  // S[t][m]: keys 16t + 4g + 0..3 of value channel 16m + i16
     u32x4 vf[2][NM];  // value channel 16m + i16 of rows 32h + 4g + 0..3 and 32h + 16 + 4g + 0..3
     float g2, aC, gamma;
@@ -173,19 +216,24 @@ struct Wave {
     // row of element e of a transposed fragment, within its 32 rows
     __device__ __forceinline__ int row_of(int e) const { return 4 * g + (e & 3) + 16 * (e >> 2); }
 
-    // channels 16x + i16 of rows 32h + .. of a tile of COLS channels
-    template <int COLS>
-    __device__ __forceinline__ u32x4 columns(const uint16_t* tile, int x, int h) const {
-        const int row = 4 * g + i16 / 4;
-        const uint16_t* p = tile + row * COLS + (((2 * x + (i16 % 4) / 2) ^ swizzle<COLS>(row)) * 8 + 4 * (i16 % 2)) + 32 * h * COLS;
-        const u32x2 lo = load_tr(p), hi = load_tr(p + 16 * COLS);
-        return u32x4{lo.x, lo.y, hi.x, hi.y};
-    }
     __device__ __forceinline__ void load_values(const uint16_t* lv, int col0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV>(lv, col0 / 16 + m, h);
+            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
+    }
+
+    // The bf16 copy for the row waves: a row of DK keys for each value channel, from row row0 on.
+    __device__ __forceinline__ void publish(uint16_t* ls, int row0) const {
+        const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
+        uint16_t* p = ls + (row0 + i16) * DK + 4 * (g % 2);
+        const int sw = swizzle<DK>(i16);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                *reinterpret_cast<u32x2*>(p + 16 * m * DK + ((2 * t + g / 2) ^ sw) * 8) =
+                    u32x2{pack_bf16x2(S[t][m][0], S[t][m][1]), pack_bf16x2(S[t][m][2], S[t][m][3])};
     }
 
     // S = S * keep + k^T (weight * v), where row j of the chunk (n rows) has weight gamma * a^(n-shift-j) *
@@ -193,6 +241,7 @@ struct Wave {
     // off), so the state keeps about 17 bits of every term.
     template <bool KEEP>
     __device__ __forceinline__ void update(const uint16_t* lk, const Table& tab, int n, float more) {
+        const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
         if constexpr (KEEP) {
             const float an = n == kChunk ? aC : power(g2, n);
 #pragma unroll
@@ -212,7 +261,7 @@ struct Wave {
             if (n < kChunk) {  // rows past the end hold zeros; their weight only has to be finite
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int left = n - shift - 32 * h - row_of(e);
+                    const int left = n - shift - 32 * h - (4 * g + (e & 3) + 16 * (e >> 2));
                     w[e] = gamma * power(g2, left < 0 ? 0 : left) * more;
                 }
             }
@@ -231,7 +280,7 @@ struct Wave {
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const u32x4 kf = columns<DK>(lk, t, h);
+                const u32x4 kf = columns<DK, false>(lk, t, h, i16, g);
 #pragma unroll
                 for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf, lo[m], S[t][m]);
 #pragma unroll
@@ -241,204 +290,182 @@ struct Wave {
     }
 };
 
-// The same value, unknown to the compiler: what is computed from it is computed in place. (LDS addresses
-// kept from chunk to chunk cost the walk registers that it had to spill.)
-__device__ __forceinline__ int anew(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
-// p^T = k q^T with its decays, rows 16w + i16 of q, to LDS.
-template <int DK>
-__device__ __forceinline__ void scores(const uint16_t* lq, const uint16_t* lk, uint16_t* lp, int w, const Table& tab, int i16,
-                                       int g) {
-    constexpr int NK = DK / 32;
-    i16 = anew(i16);
-    const int sw = swizzle<DK>(i16);
-    u32x4 qf[NK];
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk)
-        qf[kk] = *reinterpret_cast<const u32x4*>(lq + (16 * w + i16) * DK + ((4 * kk + g) ^ sw) * 8);
-#pragma unroll
-    for (int back = 0; back < 4; ++back) {
-        const int jb = w - back;
-        if (jb >= 0) {
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
-                acc = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * DK + ((4 * kk + g) ^ sw) * 8), qf[kk], acc);
-            float p[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int apart = 16 * back + i16 - 4 * g - r;
-                p[r] = acc[r] * tab.score[back == 0 && apart < 0 ? 0 : apart];
-                if (back == 0 && apart < 0) p[r] = 0.0f;  // a later row's product is dropped, whatever it holds
-            }
-            *reinterpret_cast<u32x2*>(lp + (16 * w + i16) * kPitchP + 16 * jb + 4 * g) =
-                u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
-        }
-    }
-}
-
-// o^T = S^T q^T: O[b][m] holds value channels 16m + 4g + 0..3 of row 16b + i16. The state is rounded to
-// bf16 as a matrix operand (a relative 2^-9 of each entry, as the products' other operand has; the
-// state itself stays in 32 bits).
-template <int DK, int NV, int COLSV>
-__device__ __forceinline__ void from_state(const Wave<DK, NV, COLSV>& w, const uint16_t* lq, const Table& tab,
-                                           f32x4 (&O)[4][NV / 16]) {
-    constexpr int NM = NV / 16, NK = DK / 32;
-    const int sw = swizzle<DK>(w.i16);
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int m = 0; m < NM; ++m) O[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-        u32x4 sf[NM];
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const f32x4 x = w.S[2 * kk][m], y = w.S[2 * kk + 1][m];
-            sf[m] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-        }
-        const uint16_t* row = lq + w.i16 * DK + 4 * (w.g % 2);
-        const int c = 4 * kk + w.g / 2;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + (c ^ sw) * 8 + 16 * b * DK);
-            const u32x2 hi = *reinterpret_cast<const u32x2*>(row + ((c + 2) ^ sw) * 8 + 16 * b * DK);
-            const u32x4 qt = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-            for (int m = 0; m < NM; ++m) O[b][m] = mfma(sf[m], qt, O[b][m]);
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const float carry = tab.carry[16 * b + w.i16];
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) O[b][m][r] *= carry;
-    }
-}
-
-// O += v^T p^T.
-template <int DK, int NV, int COLSV>
-__device__ __forceinline__ void from_rows(const Wave<DK, NV, COLSV>& w, const uint16_t* lp, const uint16_t* lv, int col0,
-                                          f32x4 (&O)[4][NV / 16]) {
-    constexpr int NM = NV / 16;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        f32x4 enter[NM];
-        float sum = 0.0f;
-        const uint16_t* row = lp + (16 * b + w.i16) * kPitchP;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) enter[m] = O[b][m];
-#pragma unroll
-        for (int h = 0; h <= b / 2; ++h) {
-            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 32 * h + 4 * w.g);
-            const u32x2 hi = *reinterpret_cast<const u32x2*>(row + 32 * h + 16 + 4 * w.g);
-            const u32x4 pf = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-            for (int m = 0; m < NM; ++m) O[b][m] = mfma(w.vf[h][m], pf, O[b][m]);
-        }
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(O[b][m][r], 0.0f, sum);
-        // An infinity or NaN in a later row of v meets p's zeros above the diagonal and would make NaN of
-        // rows that do not depend on it: such rows are summed again without them.
-        if (__builtin_expect(__builtin_amdgcn_ballot_w64(sum != 0.0f) != 0, 0)) {
-#pragma unroll
-            for (int m = 0; m < NM; ++m) O[b][m] = enter[m];
-#pragma clang loop unroll(disable)
-            for (int j = 0; j <= 16 * b + w.i16; ++j) {
-                const float pj = bf16_lo(row[j]);
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    const int c = col0 + 16 * m + 4 * w.g;
-                    const uint16_t* v = lv + j * COLSV + ((c / 8) ^ swizzle<COLSV>(j)) * 8 + c % 8;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) O[b][m][r] = __builtin_fmaf(pj, bf16_lo(v[r]), O[b][m][r]);
-                }
-            }
-        }
-    }
-}
-
-// Where a wave's rows of o go, addressed like the operands' from each chunk's lowest row. bf16 rows whose
-// channels go out four at a time are kept packed and stored one chunk late, before the next chunk's
-// loads are issued: stores count with the loads that a wave waits for, and a store waited for right after
-// its issue held up every chunk.
-template <int NV>
-struct Output {
-    static constexpr int NM = NV / 16;
-    char* p;  // the row before the walk's first chunk's lowest
+// What a row wave holds of its 16 rows: row 16w + i16 as fragments, natural order of channels.
+template <int DK, int VEC>
+struct RowLoads {
+    static constexpr int NK = DK / 32;
+    u32x4 f[NK];
+    const uint16_t* p;  // lowest row of the next chunk
     int64_t step;
-    u32x2 held[4][NM];
+    uint32_t off[NK];
+    int have, row;
+
+    __device__ __forceinline__ void open(const uint16_t* first_row, const Rows& x, bool reverse, int w, int i16, int g) {
+        row = 16 * w + i16;
+        p = reverse ? first_row - (kChunk - 1) * x.st : first_row;
+        step = reverse ? -kChunk * x.st : kChunk * x.st;
+        const int st = static_cast<int>(x.st);
+        have = x.dim - 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+            off[kk] = have - 32 * kk <= 0 ? kNowhere
+                                          : static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * st + 32 * kk + 8 * g) * 2);
+    }
+    __device__ __forceinline__ void load(int n) {
+        const __amdgpu_buffer_rsrc_t b = chunk_rsrc(p);
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) f[kk] = load8<VEC>(b, row < n ? off[kk] : kNowhere, 0, have - 32 * kk);
+        p += step;
+    }
+};
+
+// Where a row wave's rows of o go, addressed like the operands' from each chunk's lowest row. bf16 rows
+// whose channels go out four at a time are kept packed and stored one chunk late, before the next loads
+// are issued: stores count with the loads that a wave waits for, so a store issued after them would be
+// waited for with them.
+template <int DV>
+struct Output {
+    static constexpr int NM = DV / 16;
+    char* p;
+    int64_t step;
+    u32x2 held[NM];
     int held_rows;
-    uint32_t off[NM];
-    int st16, es, vec, dim, dv, i16;
-    bool f32, up;
+    uint32_t off;
+    int es, vec, left, row;  // left: channels from the lane's first on
+    bool f32;
 
     __device__ __forceinline__ void open(void* o, int64_t head_off, int64_t row0, int64_t o_st, int o_f32, int o_vec, bool reverse,
-                                         int dim_, int dv_, int i16_, int g) {
-        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, dim = dim_, dv = dv_ + 4 * g, i16 = i16_, up = !reverse;
+                                         int dim, int dv0, int w, int i16, int g) {
+        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, left = dim - dv0 - 4 * g, row = 16 * w + i16;
         p = static_cast<char*>(o) + (head_off + (reverse ? row0 - (kChunk - 1) : row0) * o_st) * es;
         step = (reverse ? -kChunk : kChunk) * o_st * es;
-        const int st = static_cast<int>(o_st) * es;
-        st16 = 16 * st;
         held_rows = 0;
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-            off[m] = dv + 16 * m < dim ? static_cast<uint32_t>((reverse ? 15 - i16 : i16) * st + (dv + 16 * m) * es) : kNowhere;
+        off = static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * static_cast<int>(o_st) + dv0 + 4 * g) * es);
     }
     __device__ __forceinline__ void flush() {
         if (held_rows == 0) return;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
         p += step;
+        const uint32_t at = row < held_rows ? off : kNowhere;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int m = 0; m < NM; ++m)
-                __builtin_amdgcn_raw_buffer_store_b64(held[b][m], ob, 16 * b + i16 < held_rows ? off[m] : kNowhere,
-                                                      (up ? b : 3 - b) * st16, 0);
+        for (int m = 0; m < NM; ++m)
+            __builtin_amdgcn_raw_buffer_store_b64(held[m], ob, 16 * m < left ? at + 32 * m : kNowhere, 0, 0);
         held_rows = 0;
     }
-    __device__ __forceinline__ void put(const f32x4 (&O)[4][NM], int n) {
+    __device__ __forceinline__ void put(const f32x4 (&O)[NM], int n) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int m = 0; m < NM; ++m)
-                held[b][m] = u32x2{pack_bf16x2(O[b][m][0], O[b][m][1]), pack_bf16x2(O[b][m][2], O[b][m][3])};
+        for (int m = 0; m < NM; ++m) held[m] = u32x2{pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3])};
         held_rows = n;
         if (vec == 4 && !f32) return;
         held_rows = 0;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
         p += step;
+        const bool in = row < n;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int sb = (up ? b : 3 - b) * st16;
-            const bool in = 16 * b + i16 < n;
+        for (int m = 0; m < NM; ++m) {
+            if (vec == 4) {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[m]), ob,
+                                                       in && 16 * m < left ? off + 64 * m : kNowhere, 0, 0);
+            } else {
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const uint32_t at = in ? off[m] : kNowhere;
-                if (vec == 4) {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[b][m]), ob, at, sb, 0);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t e = dv + 16 * m + r < dim ? at + r * es : kNowhere;
-                        if (f32)
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[b][m][r]), ob, e, sb, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(held[b][m][r / 2] >> (16 * (r % 2))), ob,
-                                                                  e, sb, 0);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t e = in && 16 * m + r < left ? off + (16 * m + r) * es : kNowhere;
+                    if (f32)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[m][r]), ob, e, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(held[m][r / 2] >> (16 * (r % 2))), ob, e, 0, 0);
                 }
             }
         }
     }
 };
+
+// The outputs of 16 rows of a chunk (rows 16w + i16): O[m] holds value channels 16m + 4g + 0..3.
+//   lk, lv  the chunk's keys and values; ls the state's copy, a row of DK keys for each value channel, or,
+//           with FLIP, a row of DV value channels for each key
+template <int DK, int DV, bool FLIP>
+__device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* lv, const uint16_t* ls, const Table& tab,
+                                            const u32x4 (&qf)[DK / 32], int w, int lane, bool special,
+                                            f32x4 (&O)[DV / 16]) {
+    constexpr int NK = DK / 32, NM = DV / 16;
+    lane = anew(lane);
+    const int i16 = lane % 16, g = lane / 16;
+    const int sw = swizzle<DK>(i16);
+    // p^T = k q^T with its decays: p[jb] holds rows 16jb + 4g + 0..3 of row 16w + i16
+    u32x2 p[4];
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+        p[jb] = u32x2{0u, 0u};
+        if (jb > w) continue;
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+            acc = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * DK + ((4 * kk + g) ^ sw) * 8), qf[kk], acc);
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int apart = 16 * (w - jb) + i16 - 4 * g - r;
+            x[r] = acc[r] * tab.score[apart < 0 ? 0 : apart];
+            if (apart < 0) x[r] = 0.0f;  // a later row's product is dropped, whatever it holds
+        }
+        p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    }
+    // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (a relative 2^-9 of each
+    // entry, as the products' other operand has; the state itself stays in 32 bits).
+    const float carry = tab.carry[16 * w + i16];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            u32x4 sf;
+            if constexpr (FLIP)
+                sf = columns<DV, true>(ls, m, kk, i16, g);
+            else
+                sf = *reinterpret_cast<const u32x4*>(ls + (16 * m + i16) * DK + ((4 * kk + g) ^ sw) * 8);
+            acc = mfma(sf, qf[kk], acc);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[m][r] = acc[r] * carry;
+    }
+    // o^T += v^T p^T. Of the 32 rows that hold the wave's own 16, those after them are left out. Where
+    // the chunk's values hold infinities or NaN, so are, row by row, the later ones among its own: they
+    // would meet p's zeros and make NaN of rows that do not depend on them.
+    const int own = w / 2;
+    const bool odd = w % 2;
+    if (own == 1) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            O[m] = mfma(columns<DV, false>(lv, m, 0, i16, g), u32x4{p[0].x, p[0].y, p[1].x, p[1].y}, O[m]);
+    }
+    const u32x2 pa = own ? p[2] : p[0], pb = own ? p[3] : p[1], none = {0u, 0u};
+    const u32x4 pf = {pa.x, pa.y, pb.x, pb.y};
+    if (__builtin_expect(!special, 1)) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const u32x2 va = half_columns<DV>(lv, m, 32 * own, i16, g);
+            const u32x2 vb = odd ? half_columns<DV>(lv, m, 32 * own + 16, i16, g) : none;
+            O[m] = mfma(u32x4{va.x, va.y, vb.x, vb.y}, pf, O[m]);
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const u32x2 mine = half_columns<DV>(lv, m, 16 * w, i16, g);
+            if (odd) {  // the earlier 16 rows as they are
+                const u32x2 va = half_columns<DV>(lv, m, 32 * own, i16, g);
+                O[m] = mfma(u32x4{va.x, va.y, 0u, 0u}, pf, O[m]);
+            }
+#pragma clang loop unroll(disable)
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t keep = g != j / 4 ? 0u : j % 2 ? 0xffff0000u : 0xffffu;
+                const uint32_t x = j % 4 < 2 ? mine.x & keep : 0u, y = j % 4 < 2 ? 0u : mine.y & keep;
+                const f32x4 next = mfma(odd ? u32x4{0u, 0u, x, y} : u32x4{x, y, 0u, 0u}, pf, O[m]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) O[m][r] = i16 >= j ? next[r] : O[m][r];
+            }
+        }
+    }
+}
 
 // The segment a workgroup works on. False: nothing to do.
 struct Segment {
@@ -508,81 +535,209 @@ __device__ __forceinline__ void store_matrix(const Wave<DK, NV, COLSV>& w, float
 
 }  // namespace
 
-// The walk. Four waves, NV value channels each.
-template <int DK, int NV, int VEC>
-__global__ __launch_bounds__(256, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
-    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
-    __shared__ __align__(16) uint16_t lq[kChunk * DK];
-    __shared__ __align__(16) uint16_t lk[kChunk * DK];
-    __shared__ __align__(16) uint16_t lv[kChunk * DVB];
-    __shared__ __align__(16) uint16_t lp[kChunk * kPitchP];
-    __shared__ Table tab;
-
-    if (a.status && *a.status != CCONV_OK) return;
-    Segment s;
-    if (!s.open(a)) return;
-    const int64_t row0 = s.row0(a.reverse);
-    Stage<DK, VEC, 256> sq, sk;
-    Stage<DVB, VEC, 256> sv;
-    sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
-    sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
-    sq.open(s.row(a, a.q, row0), a.q, a.reverse, 0);
-    int n = static_cast<int>(s.rows < kChunk ? s.rows : kChunk);
-    sk.load(n);
-    sv.load(n);
-    sq.load(n);
-
-    const int wave = wave_id(), lane = threadIdx.x % kWave;
-    Wave<DK, NV, DVB> w;
-    w.open(a.log_decay[s.hv], a.gamma, a.shift);
-    tab.fill(w.g2, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
-    const int dv0 = s.vb * DVB + wave * NV;
-    const int64_t matrix = (s.seq * a.HV + s.hv) * static_cast<int64_t>(a.k.dim) * a.v.dim;
+// The state that enters a segment.
+template <int DK, int NV, int COLSV>
+__device__ __forceinline__ void enter(Wave<DK, NV, COLSV>& w, const WalkArgs& a, const Segment& s, int wave, int lane) {
+    constexpr int NT = DK / 16, NM = NV / 16;
     if (s.first > 0) {
-        const float* c = a.states + ((s.seg - 1) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB +
-                         s.vb * DK * DVB + (wave * 64 + lane) * 4;
+        const float* c = a.states + ((s.seg - 1) * a.sub * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * 4 * NV +
+                         s.vb * DK * 4 * NV + (wave * 64 + lane) * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int m = 0; m < NM; ++m) w.S[t][m] = *reinterpret_cast<const f32x4*>(c + (t * NM + m) * 1024);
     }
     if (a.init)
-        add_matrix(w, a.init + matrix, power_long(a.log_decay[s.hv], s.first), a.k.dim, a.v.dim, dv0, a.sk, a.sv);
-    Output<NV> out;
-    out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, dv0, w.i16, w.g);
-    // p's tiles above the diagonal are read by the 32-row products and stay zero
-    for (int i = threadIdx.x; i < kChunk * kPitchP / 2; i += 256) reinterpret_cast<uint32_t*>(lp)[i] = 0u;
+        add_matrix(w, a.init + (s.seq * a.HV + s.hv) * static_cast<int64_t>(a.k.dim) * a.v.dim,
+                   power_long(a.log_decay[s.hv], s.first), a.k.dim, a.v.dim, s.vb * 4 * NV + wave * NV, a.sk, a.sv);
+}
 
-    const int rows = static_cast<int>(s.rows);
-    for (int c0 = 0; c0 < rows; c0 += kChunk) {
-        lds_barrier();  // the chunk before has been read
-        sk.store(lk);
-        sv.store(lv);
-        sq.store(lq);
+// The walk: four row waves, then four state waves, of NV value channels each.
+template <int DK, int NV, int VEC>
+__global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
+    constexpr int DVB = 4 * NV;
+    __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
+    __shared__ __align__(16) uint16_t lv[2][kChunk * DVB];
+    __shared__ __align__(16) uint16_t ls[2][DVB * DK];
+    __shared__ Table tab;
+    __shared__ int odd_chunk[2];  // a chunk whose values hold an infinity or NaN
+
+    if (a.status && *a.status != CCONV_OK) return;
+    Segment s;
+    if (!s.open(a)) return;
+    const int64_t row0 = s.row0(a.reverse);
+    const int rows = static_cast<int>(s.rows), wave = wave_id(), lane = threadIdx.x % kWave, i16 = lane % 16, g = lane / 16;
+    Stage<DK, VEC, 512> sk;
+    Stage<DVB, VEC, 512> sv;
+    sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+    sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
+    sk.load(rows);
+    sv.load(rows);
+    tab.fill(a.log_decay[s.hv] * 1.4426950408889634f, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
+    auto stage = [&](int c0) {  // chunk c0 from registers to LDS
+        const int b = (c0 / kChunk) & 1;
+        sk.store(lk[b]);
+        sv.store(lv[b]);
+        if (sv.special()) odd_chunk[b] = c0;
+    };
+    auto special = [&](int c0) { return __builtin_amdgcn_readfirstlane(odd_chunk[(c0 / kChunk) & 1]) == c0; };
+    if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
+    __syncthreads();
+    auto ahead = [&](int left) {
+        if (left <= 0) return;
+        sk.load(left);
+        sv.load(left);
+    };
+    if (wave < 4) {
+        RowLoads<DK, VEC> q;
+        q.open(s.row(a, a.q, row0), a.q, a.reverse, wave, i16, g);
+        q.load(rows);
+        Output<DVB> out;
+        out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, s.vb * DVB, wave, i16,
+                 g);
+        stage(0);
+        ahead(rows - kChunk);
         lds_barrier();
-        out.flush();
-        n = rows - c0 < kChunk ? rows - c0 : kChunk;
-        if (rows - c0 > kChunk) {
-            sk.load(rows - c0 - kChunk);
-            sv.load(rows - c0 - kChunk);
-            sq.load(rows - c0 - kChunk);
+        for (int c0 = 0; c0 < rows; c0 += kChunk) {
+            const int b = (c0 / kChunk) & 1, left = rows - c0;
+            u32x4 qf[DK / 32];
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk) qf[kk] = q.f[kk];
+            if (left > kChunk) stage(c0 + kChunk);
+            out.flush();
+            ahead(left - 2 * kChunk);
+            if (left > kChunk) q.load(left - kChunk);
+            f32x4 O[DVB / 16];
+            row_outputs<DK, DVB, false>(lk[b], lv[b], ls[b], tab, qf, wave, lane, special(c0), O);
+            out.put(O, left < kChunk ? left : kChunk);
+            lds_barrier();
         }
-        scores<DK>(lq, lk, lp, wave, tab, w.i16, w.g);
-        f32x4 O[4][NM];
-        from_state(w, lq, tab, O);
-        w.load_values(lv, wave * NV);
-        lds_barrier();  // p is whole
-        from_rows(w, lp, lv, wave * NV, O);
-        out.put(O, n);
-        w.template update<true>(lk, tab, n, 1.0f);
+        out.flush();
+    } else {
+        const int w4 = wave - 4;
+        Wave<DK, NV, DVB> w;
+        w.open(a.log_decay[s.hv], a.gamma, a.shift);
+        enter(w, a, s, w4, lane);
+        stage(0);
+        ahead(rows - kChunk);
+        w.publish(ls[0], w4 * NV);
+        lds_barrier();
+        for (int c0 = 0; c0 < rows; c0 += kChunk) {
+            const int b = (c0 / kChunk) & 1, left = rows - c0;
+            if (left > kChunk) stage(c0 + kChunk);
+            ahead(left - 2 * kChunk);
+            w.load_values(lv[b], w4 * NV);
+            w.template update<true>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
+            if (left > kChunk) w.publish(ls[b ^ 1], w4 * NV);
+            lds_barrier();
+        }
+        if (s.last && a.fin)
+            store_matrix(w, a.fin + (s.seq * a.HV + s.hv) * static_cast<int64_t>(a.k.dim) * a.v.dim, a.k.dim, a.v.dim,
+                         s.vb * DVB + w4 * NV, a.sk, a.sv);
     }
-    out.flush();
-    if (s.last && a.fin) store_matrix(w, a.fin + matrix, a.k.dim, a.v.dim, dv0, a.sk, a.sv);
+}
+
+// Two walks over the same rows whose states are each other's transposes: dv (rows k, keys q, values do)
+// and dk (rows v, keys do, values q). One set of state waves serves both, the second set of row waves
+// reading the state's copy by columns; q and do are staged once.
+template <int DK, int DV, int VEC>
+__global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a, SecondWalk z) {
+    constexpr int NV = DV / 4;
+    __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
+    __shared__ __align__(16) uint16_t lv[2][kChunk * DV];
+    __shared__ __align__(16) uint16_t ls[2][DV * DK];
+    __shared__ Table tab;
+    __shared__ int odd_chunk[2];  // a chunk whose values hold an infinity or NaN
+
+    if (a.status && *a.status != CCONV_OK) return;
+    Segment s;
+    if (!s.open(a)) return;
+    const int64_t row0 = s.row0(a.reverse);
+    const int rows = static_cast<int>(s.rows), wave = wave_id(), lane = threadIdx.x % kWave, i16 = lane % 16, g = lane / 16;
+    tab.fill(a.log_decay[s.hv] * 1.4426950408889634f, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
+    if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
+    __syncthreads();
+    if (wave < 8) {
+        Stage<DK, VEC, 512> sk;
+        Stage<DV, VEC, 512> sv;
+        sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+        sv.open(s.row(a, a.v, row0), a.v, a.reverse, 0);
+        sk.load(rows);
+        sv.load(rows);
+        auto stage = [&](int c0) {
+            const int b = (c0 / kChunk) & 1;
+            sk.store(lk[b]);
+            sv.store(lv[b]);
+            if (sk.special() || sv.special()) odd_chunk[b] = c0;
+        };
+        auto special = [&](int c0) { return __builtin_amdgcn_readfirstlane(odd_chunk[(c0 / kChunk) & 1]) == c0; };
+        auto ahead = [&](int left) {
+            if (left <= 0) return;
+            sk.load(left);
+            sv.load(left);
+        };
+        auto walk = [&](auto& q, auto& out, auto&& outputs) {
+            q.load(rows);
+            stage(0);
+            ahead(rows - kChunk);
+            lds_barrier();
+            for (int c0 = 0; c0 < rows; c0 += kChunk) {
+                const int b = (c0 / kChunk) & 1, left = rows - c0;
+                auto qf = q;
+                if (left > kChunk) stage(c0 + kChunk);
+                out.flush();
+                ahead(left - 2 * kChunk);
+                if (left > kChunk) q.load(left - kChunk);
+                outputs(b, qf.f, left < kChunk ? left : kChunk, special(c0));
+                lds_barrier();
+            }
+            out.flush();
+        };
+        if (wave < 4) {
+            RowLoads<DK, VEC> q;
+            Output<DV> out;
+            q.open(s.row(a, a.q, row0), a.q, a.reverse, wave, i16, g);
+            out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, 0, wave, i16, g);
+            walk(q, out, [&](int b, const u32x4(&f)[DK / 32], int n, bool odd) {
+                f32x4 O[DV / 16];
+                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], tab, f, wave, lane, odd, O);
+                out.put(O, n);
+            });
+        } else {
+            RowLoads<DV, VEC> q;
+            Output<DK> out;
+            q.open(s.row(a, z.q, row0), z.q, a.reverse, wave - 4, i16, g);
+            out.open(z.o, s.batch(a) * z.o_sb + s.hv * z.o_sh, row0, z.o_st, z.o_f32, z.o_vec, a.reverse, a.k.dim, 0, wave - 4, i16, g);
+            walk(q, out, [&](int b, const u32x4(&f)[DV / 32], int n, bool odd) {
+                f32x4 O[DK / 16];
+                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], tab, f, wave - 4, lane, odd, O);
+                out.put(O, n);
+            });
+        }
+    } else {
+        const int w4 = wave - 8;
+        Wave<DK, NV, DV> w;
+        w.open(a.log_decay[s.hv], a.gamma, a.shift);
+        enter(w, a, s, w4, lane);
+        w.publish(ls[0], w4 * NV);
+        lds_barrier();
+        for (int c0 = 0; c0 < rows; c0 += kChunk) {
+            const int b = (c0 / kChunk) & 1, left = rows - c0;
+            w.load_values(lv[b], w4 * NV);
+            w.template update<true>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
+            if (left > kChunk) w.publish(ls[b ^ 1], w4 * NV);
+            lds_barrier();
+        }
+        if (s.last && a.fin)
+            store_matrix(w, a.fin + (s.seq * a.HV + s.hv) * static_cast<int64_t>(a.k.dim) * a.v.dim, a.k.dim, a.v.dim, w4 * NV, a.sk,
+                         a.sv);
+    }
 }
 
 // Each segment's own sum of k^T v, for the segments that another follows. The chunks are taken from the
 // segment's last to its first: their weights then only grow smaller, so the state needs no scaling, and
-// the rows read last are those that the walk after it reads first.
+// the rows read last are those that the walk after it reads first. A segment is summed in `sub` parts, each
+// by a workgroup of its own.
 template <int DK, int NV, int VEC>
 __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
@@ -592,9 +747,10 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
 
     if (a.status && *a.status != CCONV_OK) return;
     Segment s;
+    const int part = static_cast<int>(blockIdx.y);
     if (!s.open(a) || s.last) return;  // (so the segment is whole)
-    const int rows = static_cast<int>(s.rows);
-    const int64_t row0 = s.row0(a.reverse) + (a.reverse ? -(rows - kChunk) : rows - kChunk);
+    const int rows = static_cast<int>(s.rows) / a.sub, end = rows * (part + 1) - kChunk;
+    const int64_t row0 = s.row0(a.reverse) + (a.reverse ? -end : end);
     Stage<DK, VEC, 256> sk;
     Stage<DVB, VEC, 256> sv;
     sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
@@ -620,7 +776,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
         w.template update<false>(lk, tab, kChunk, more);
         more *= w.aC;
     }
-    float* c = a.states + (s.seg * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
+    float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
                (wave * 64 + lane) * 4;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -628,7 +784,8 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
         for (int m = 0; m < NM; ++m) *reinterpret_cast<f32x4*>(c + (t * NM + m) * 1024) = w.S[t][m];
 }
 
-// One workgroup per (sequence, head, 1024 floats): the running sum over the sequence's segments.
+// One workgroup per (sequence, head, 1024 floats): the running sum over the parts of the sequence's
+// segments, left in a segment's first part's place after its last.
 __global__ __launch_bounds__(256) void cconv_linattn_scan_kernel(ScanArgs a) {
     if (a.status && *a.status != CCONV_OK) return;
     const int64_t parts = a.floats / 1024;
@@ -639,22 +796,22 @@ __global__ __launch_bounds__(256) void cconv_linattn_scan_kernel(ScanArgs a) {
     } else {
         s0 = seq * a.segs, s1 = s0 + a.segs;
     }
-    const float w = power_long(a.log_decay[hv], a.seg_rows);
-    f32x4* p = reinterpret_cast<f32x4*>(a.states + (s0 * a.HV + hv) * a.floats + part * 1024) + threadIdx.x;
-    const int64_t step = a.HV * a.floats / 4;
+    const float w = power_long(a.log_decay[hv], a.seg_rows / a.sub);
+    f32x4* p = reinterpret_cast<f32x4*>(a.states + (s0 * a.sub * a.HV + hv) * a.floats + part * 1024) + threadIdx.x;
+    const int64_t step = a.HV * a.floats / 4, n = (s1 - s0 - 1) * a.sub;
     f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kAhead = 8;  // loads in flight
-    for (int64_t s = s0; s + 1 < s1; s += kAhead, p += kAhead * step) {
+    constexpr int kAhead = 8;  // loads in flight (a multiple of sub)
+    for (int64_t k = 0; k < n; k += kAhead, p += kAhead * step) {
         f32x4 x[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (s + i + 1 < s1) x[i] = p[i * step];
+            if (k + i < n) x[i] = p[i * step];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (s + i + 1 >= s1) break;
+            if (k + i >= n) break;
 #pragma unroll
             for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(w, c[r], x[i][r]);
-            p[i * step] = c;
+            if ((i + 1) % a.sub == 0) p[(i + 1 - a.sub) * step] = c;
         }
     }
 }
@@ -736,11 +893,11 @@ WalkShape walk_shape(int64_t Dk, int64_t Dv) {
 
 template <int DK, int NV, int VEC>
 static hipError_t walk_go(bool states, const WalkArgs& a, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(a.segments * a.HV * a.vblocks)), block(256);
+    const uint32_t groups = static_cast<uint32_t>(a.segments * a.HV * a.vblocks);
     if (states)
-        hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), dim3(groups, a.sub), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC>), dim3(groups), dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
@@ -756,6 +913,26 @@ hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, 
     if (w.DK == 64) return w.NV == 32 ? walk_vec<64, 32>(vec, states_only, a, s) : walk_vec<64, 16>(vec, states_only, a, s);
     if (w.DK == 128) return w.NV == 32 ? walk_vec<128, 32>(vec, states_only, a, s) : walk_vec<128, 16>(vec, states_only, a, s);
     return walk_vec<256, 16>(vec, states_only, a, s);
+}
+
+template <int DK, int DV>
+static hipError_t walk2_vec(int vec, const WalkArgs& a, const SecondWalk& z, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(a.segments * a.HV)), block(768);
+    if (vec == 8)
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 8>), grid, block, 0, s, a, z);
+    else if (vec == 4)
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 4>), grid, block, 0, s, a, z);
+    else
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 1>), grid, block, 0, s, a, z);
+    return hipGetLastError();
+}
+
+hipError_t launch_walk2(const WalkShape& w, const WalkArgs& a, const SecondWalk& z, hipStream_t s) {
+    int vec = a.k.vec < a.v.vec ? a.k.vec : a.v.vec;
+    if (a.q.vec < vec) vec = a.q.vec;
+    if (z.q.vec < vec) vec = z.q.vec;
+    if (w.DK == 64) return w.NV == 32 ? walk2_vec<64, 128>(vec, a, z, s) : walk2_vec<64, 64>(vec, a, z, s);
+    return w.NV == 32 ? walk2_vec<128, 128>(vec, a, z, s) : walk2_vec<128, 64>(vec, a, z, s);
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
