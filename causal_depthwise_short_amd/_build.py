@@ -23,7 +23,7 @@ CFLAGS = [
     f"--offload-arch={ARCH}",
     "-O3",
     "-fPIC",
-    "-std=c++17",
+    "-std=c++20",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",

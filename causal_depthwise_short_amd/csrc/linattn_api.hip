@@ -296,7 +296,7 @@ cconv_status_t cconv_linattn_fwd(const cconv_rows_t* q, const cconv_rows_t* k, c
     a.v = rows_of(*v, dv, 1);
     a.o = const_cast<void*>(o->p);
     a.o_sb = o->sb, a.o_st = T > 1 ? o->st : 0, a.o_sh = o->sh;
-    a.o_vec = row_vec(*o, dv) >= 4 ? 4 : 1;
+    a.o_vec = row_vec(*o, dv);
     a.log_decay = log_decay;
     a.alpha = a.beta = scale, a.gamma = 1.0f;
     a.shift = 1;
@@ -371,7 +371,7 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
             a.o = const_cast<void*>(r.p);
             a.o_sb = r.sb, a.o_st = T > 1 ? r.st : 0, a.o_sh = r.sh;
             a.o_f32 = 0;
-            a.o_vec = row_vec(r, d) >= 4 ? 4 : 1;
+            a.o_vec = row_vec(r, d);
         } else {
             a.o = p.part;
             a.o_sh = d.dim, a.o_st = HV * d.dim, a.o_sb = T * a.o_st;  // at most 2^22, as a caller's

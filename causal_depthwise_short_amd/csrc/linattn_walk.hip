@@ -57,6 +57,10 @@ __device__ __forceinline__ float power_long(float g, int64_t n) {
 constexpr uint32_t kNowhere = 0x80000000u;
 constexpr int kRange = 0x7fffffff;
 
+// A register set or buffer by number, known at compile time.
+template <int N>
+struct Set {};
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, kRange, 0x00020000);
 }
@@ -116,8 +120,9 @@ struct Stage {
     bool up;
 
     __device__ __forceinline__ void open(const uint16_t* first_row, const Rows& x, bool reverse, int col0) {
-        row = threadIdx.x / kPerRow;
-        const int col = col0 + (threadIdx.x % kPerRow) * 8;
+        const int i = threadIdx.x % THREADS;  // (the last THREADS threads of a workgroup stage, or all)
+        row = i / kPerRow;
+        const int col = col0 + i % kPerRow * 8;
         have = x.dim - col;
         up = !reverse;
         p = reverse ? first_row - (kChunk - 1) * x.st : first_row;
@@ -181,16 +186,14 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 
-// Powers of the decay in LDS, the same for every chunk (held in registers, they made the walk spill).
+// LDS loads written above stay above: the scheduler, minding registers, would put each right before its use.
+__device__ __forceinline__ void loads_first() { __builtin_amdgcn_sched_barrier(0x7f); }
+
+// Weights of a full chunk's rows in the state, gamma * a^(64 - shift - r), in LDS.
 struct Table {
-    alignas(16) float score[kChunk];   // alpha * a^n: scores of rows n apart
-    alignas(16) float carry[kChunk];   // beta * a^(r + shift): what the state gives row r
-    alignas(16) float weight[kChunk];  // gamma * a^(64 - shift - r): row r of a full chunk in the state
-    __device__ __forceinline__ void fill(float g2, float alpha, float beta, float gamma, int shift, int i) {
-        if (i >= kChunk) return;
-        score[i] = alpha * power(g2, i);
-        carry[i] = beta * power(g2, i + shift);
-        weight[i] = gamma * power(g2, kChunk - shift - i);
+    alignas(16) float weight[kChunk];
+    __device__ __forceinline__ void fill(float log_decay, float gamma, int shift, int i) {
+        if (i < kChunk) weight[i] = gamma * power(log_decay * 1.4426950408889634f, kChunk - shift - i);
     }
 };
 
@@ -239,9 +242,15 @@ struct Wave {
     // S = S * keep + k^T (weight * v), where row j of the chunk (n rows) has weight gamma * a^(n-shift-j) *
     // more. The weighted v is taken as a sum of two bf16 values (the second holds what the first rounds
     // off), so the state keeps about 17 bits of every term.
-    template <bool KEEP>
+    template <bool KEEP, int PRE>
     __device__ __forceinline__ void update(const uint16_t* lk, const Table& tab, int n, float more) {
         const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
+        // a half's first PRE loads are issued before its values are weighted, the second half's before the
+        // first's products: their latency is behind other work
+        u32x4 kf[2][PRE];
+#pragma unroll
+        for (int t = 0; t < PRE; ++t) kf[0][t] = columns<DK, false>(lk, t, 0, i16, g);
+        loads_first();
         if constexpr (KEEP) {
             const float an = n == kChunk ? aC : power(g2, n);
 #pragma unroll
@@ -251,6 +260,7 @@ struct Wave {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) S[t][m][r] *= an;
         }
+        u32x4 hi[NM], lo[NM];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 4 * g),
@@ -265,7 +275,6 @@ struct Wave {
                     w[e] = gamma * power(g2, left < 0 ? 0 : left) * more;
                 }
             }
-            u32x4 hi[NM], lo[NM];
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
 #pragma unroll
@@ -278,23 +287,28 @@ struct Wave {
                                            __builtin_amdgcn_fmed3f(u1 - bf16_hi(x), -1e38f, 1e38f));
                 }
             }
+            if (h == 0) {
+#pragma unroll
+                for (int t = 0; t < PRE; ++t) kf[1][t] = columns<DK, false>(lk, t, 1, i16, g);
+                loads_first();
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const u32x4 kf = columns<DK, false>(lk, t, h, i16, g);
+                const u32x4 k = t < PRE ? kf[h][t < PRE ? t : 0] : columns<DK, false>(lk, t, h, i16, g);
 #pragma unroll
-                for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf, lo[m], S[t][m]);
+                for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, lo[m], S[t][m]);
 #pragma unroll
-                for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf, hi[m], S[t][m]);
+                for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, hi[m], S[t][m]);
             }
         }
     }
 };
 
 // What a row wave holds of its 16 rows: row 16w + i16 as fragments, natural order of channels.
-template <int DK, int VEC>
+template <int DK, int VEC, int SETS = 1>
 struct RowLoads {
     static constexpr int NK = DK / 32;
-    u32x4 f[NK];
+    u32x4 f[SETS][NK];
     const uint16_t* p;  // lowest row of the next chunk
     int64_t step;
     uint32_t off[NK];
@@ -311,10 +325,11 @@ struct RowLoads {
             off[kk] = have - 32 * kk <= 0 ? kNowhere
                                           : static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * st + 32 * kk + 8 * g) * 2);
     }
+    template <int SET = 0>
     __device__ __forceinline__ void load(int n) {
         const __amdgpu_buffer_rsrc_t b = chunk_rsrc(p);
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) f[kk] = load8<VEC>(b, row < n ? off[kk] : kNowhere, 0, have - 32 * kk);
+        for (int kk = 0; kk < NK; ++kk) f[SET][kk] = load8<VEC>(b, row < n ? off[kk] : kNowhere, 0, have - 32 * kk);
         p += step;
     }
 };
@@ -331,39 +346,52 @@ struct Output {
     u32x2 held[NM];
     int held_rows;
     uint32_t off;
-    int es, vec, left, row;  // left: channels from the lane's first on
+    int es, vec, left, row, g;  // left: channels from the lane's first on
     bool f32;
 
     __device__ __forceinline__ void open(void* o, int64_t head_off, int64_t row0, int64_t o_st, int o_f32, int o_vec, bool reverse,
-                                         int dim, int dv0, int w, int i16, int g) {
-        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, left = dim - dv0 - 4 * g, row = 16 * w + i16;
+                                         int dim, int dv0, int w, int i16, int g_) {
+        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, g = g_, row = 16 * w + i16;
+        // pairs of tiles go out eight channels a lane: lane group g then has channels 16 (g % 2) + 8 (g / 2) ..
+        const int c = vec == 8 && !f32 ? 16 * (g % 2) + 8 * (g / 2) : 4 * g;
+        left = dim - dv0 - c;
         p = static_cast<char*>(o) + (head_off + (reverse ? row0 - (kChunk - 1) : row0) * o_st) * es;
         step = (reverse ? -kChunk : kChunk) * o_st * es;
         held_rows = 0;
-        off = static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * static_cast<int>(o_st) + dv0 + 4 * g) * es);
+        off = static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * static_cast<int>(o_st) + dv0 + c) * es);
     }
     __device__ __forceinline__ void flush() {
         if (held_rows == 0) return;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
         p += step;
         const uint32_t at = row < held_rows ? off : kNowhere;
+        if (vec == 8) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-            __builtin_amdgcn_raw_buffer_store_b64(held[m], ob, 16 * m < left ? at + 32 * m : kNowhere, 0, 0);
+            for (int m = 0; m < NM; m += 2) {
+                // rows of 16 lanes: the second of the first tile's against the first of the second's, and so on
+                const auto x = __builtin_amdgcn_permlane16_swap(held[m].x, held[m + 1].x, false, false);
+                const auto y = __builtin_amdgcn_permlane16_swap(held[m].y, held[m + 1].y, false, false);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], y[0], x[1], y[1]}, ob, 16 * m < left ? at + 32 * m : kNowhere, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                __builtin_amdgcn_raw_buffer_store_b64(held[m], ob, 16 * m < left ? at + 32 * m : kNowhere, 0, 0);
+        }
         held_rows = 0;
     }
     __device__ __forceinline__ void put(const f32x4 (&O)[NM], int n) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) held[m] = u32x2{pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3])};
         held_rows = n;
-        if (vec == 4 && !f32) return;
+        if (vec >= 4 && !f32) return;
         held_rows = 0;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
         p += step;
         const bool in = row < n;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            if (vec == 4) {
+            if (vec >= 4) {
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[m]), ob,
                                                        in && 16 * m < left ? off + 64 * m : kNowhere, 0, 0);
             } else {
@@ -380,42 +408,60 @@ struct Output {
     }
 };
 
+// Decays of a row wave's scores and of what the state gives, the same for every chunk.
+struct Decays {
+    float score[4][4];  // alpha * a^n for row 16w + i16 and row 16jb + 4g + r, n apart
+    float carry;        // beta * a^(16w + i16 + shift)
+    __device__ __forceinline__ void open(float log_decay, float alpha, float beta, int shift, int w, int i16, int g) {
+        const float g2 = log_decay * 1.4426950408889634f;
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int n = 16 * (w - jb) + i16 - 4 * g - r;
+                score[jb][r] = alpha * power(g2, n < 0 ? 0 : n);
+            }
+        carry = beta * power(g2, 16 * w + i16 + shift);
+    }
+};
+
 // The outputs of 16 rows of a chunk (rows 16w + i16): O[m] holds value channels 16m + 4g + 0..3.
 //   lk, lv  the chunk's keys and values; ls the state's copy, a row of DK keys for each value channel, or,
 //           with FLIP, a row of DV value channels for each key
-template <int DK, int DV, bool FLIP>
-__device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* lv, const uint16_t* ls, const Table& tab,
+//   first, second  what the wave has to issue besides, put between the products
+template <int DK, int DV, bool FLIP, class First, class Second>
+__device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* lv, const uint16_t* ls, const Decays& d,
                                             const u32x4 (&qf)[DK / 32], int w, int lane, bool special,
-                                            f32x4 (&O)[DV / 16]) {
+                                            f32x4 (&O)[DV / 16], First&& first, Second&& second) {
     constexpr int NK = DK / 32, NM = DV / 16;
     lane = anew(lane);
     const int i16 = lane % 16, g = lane / 16;
     const int sw = swizzle<DK>(i16);
-    // p^T = k q^T with its decays: p[jb] holds rows 16jb + 4g + 0..3 of row 16w + i16
+    // p^T = k q^T with its decays: p[jb] holds rows 16jb + 4g + 0..3 of row 16w + i16. All four tiles, also
+    // those of later rows, for every wave: without branches the loads run ahead of the products.
+    f32x4 acc[4];
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) acc[jb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb)
+            acc[jb] = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * DK + ((4 * kk + g) ^ sw) * 8), qf[kk], acc[jb]);
     u32x2 p[4];
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
-        p[jb] = u32x2{0u, 0u};
-        if (jb > w) continue;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk)
-            acc = mfma(*reinterpret_cast<const u32x4*>(lk + (16 * jb + i16) * DK + ((4 * kk + g) ^ sw) * 8), qf[kk], acc);
         float x[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int apart = 16 * (w - jb) + i16 - 4 * g - r;
-            x[r] = acc[r] * tab.score[apart < 0 ? 0 : apart];
-            if (apart < 0) x[r] = 0.0f;  // a later row's product is dropped, whatever it holds
-        }
+        for (int r = 0; r < 4; ++r)  // a later row's product is dropped, whatever it holds
+            x[r] = 16 * (w - jb) + i16 - 4 * g - r >= 0 ? acc[jb][r] * d.score[jb][r] : 0.0f;
         p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
+    first();
     // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (a relative 2^-9 of each
     // entry, as the products' other operand has; the state itself stays in 32 bits).
-    const float carry = tab.carry[16 * w + i16];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 at = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
             u32x4 sf;
@@ -423,45 +469,39 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
                 sf = columns<DV, true>(ls, m, kk, i16, g);
             else
                 sf = *reinterpret_cast<const u32x4*>(ls + (16 * m + i16) * DK + ((4 * kk + g) ^ sw) * 8);
-            acc = mfma(sf, qf[kk], acc);
+            at = mfma(sf, qf[kk], at);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) O[m][r] = acc[r] * carry;
+        for (int r = 0; r < 4; ++r) O[m][r] = at[r] * d.carry;
     }
-    // o^T += v^T p^T. Of the 32 rows that hold the wave's own 16, those after them are left out. Where
-    // the chunk's values hold infinities or NaN, so are, row by row, the later ones among its own: they
-    // would meet p's zeros and make NaN of rows that do not depend on them.
-    const int own = w / 2;
-    const bool odd = w % 2;
-    if (own == 1) {
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-            O[m] = mfma(columns<DV, false>(lv, m, 0, i16, g), u32x4{p[0].x, p[0].y, p[1].x, p[1].y}, O[m]);
-    }
-    const u32x2 pa = own ? p[2] : p[0], pb = own ? p[3] : p[1], none = {0u, 0u};
-    const u32x4 pf = {pa.x, pa.y, pb.x, pb.y};
+    second();
+    // o^T += v^T p^T. Where the chunk's values hold infinities or NaN, later rows are left out one by one:
+    // they would meet p's zeros and make NaN of rows that do not depend on them.
     if (__builtin_expect(!special, 1)) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const u32x2 va = half_columns<DV>(lv, m, 32 * own, i16, g);
-            const u32x2 vb = odd ? half_columns<DV>(lv, m, 32 * own + 16, i16, g) : none;
-            O[m] = mfma(u32x4{va.x, va.y, vb.x, vb.y}, pf, O[m]);
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                O[m] = mfma(columns<DV, false>(lv, m, h, i16, g), u32x4{p[2 * h].x, p[2 * h].y, p[2 * h + 1].x, p[2 * h + 1].y}, O[m]);
     } else {
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            const u32x2 mine = half_columns<DV>(lv, m, 16 * w, i16, g);
-            if (odd) {  // the earlier 16 rows as they are
-                const u32x2 va = half_columns<DV>(lv, m, 32 * own, i16, g);
-                O[m] = mfma(u32x4{va.x, va.y, 0u, 0u}, pf, O[m]);
-            }
-#pragma clang loop unroll(disable)
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t keep = g != j / 4 ? 0u : j % 2 ? 0xffff0000u : 0xffffu;
-                const uint32_t x = j % 4 < 2 ? mine.x & keep : 0u, y = j % 4 < 2 ? 0u : mine.y & keep;
-                const f32x4 next = mfma(odd ? u32x4{0u, 0u, x, y} : u32x4{x, y, 0u, 0u}, pf, O[m]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) O[m][r] = i16 >= j ? next[r] : O[m][r];
+            for (int jb = 0; jb < 4; ++jb) {
+                if (jb > w) continue;
+                const u32x2 v = half_columns<DV>(lv, m, 16 * jb, i16, g);
+                const u32x4 pf = {p[jb].x, p[jb].y, 0u, 0u};
+                if (jb < w) {
+                    O[m] = mfma(u32x4{v.x, v.y, 0u, 0u}, pf, O[m]);
+                    continue;
+                }
+#pragma clang loop unroll(disable)
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t keep = g != j / 4 ? 0u : j % 2 ? 0xffff0000u : 0xffffu;
+                    const f32x4 next = mfma(u32x4{j % 4 < 2 ? v.x & keep : 0u, j % 4 < 2 ? 0u : v.y & keep, 0u, 0u}, pf, O[m]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[m][r] = i16 >= j ? next[r] : O[m][r];
+                }
             }
         }
     }
@@ -552,10 +592,12 @@ __device__ __forceinline__ void enter(Wave<DK, NV, COLSV>& w, const WalkArgs& a,
                    power_long(a.log_decay[s.hv], s.first), a.k.dim, a.v.dim, s.vb * 4 * NV + wave * NV, a.sk, a.sv);
 }
 
-// The walk: four row waves, then four state waves, of NV value channels each.
+// The walk: four row waves, then four state waves, of NV value channels each, which also stage the chunks
+// (the row waves' part is the longer).
 template <int DK, int NV, int VEC>
 __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV;
+    constexpr int PRE = DK == 256 ? 4 : DK / 16;  // as the registers allow
     __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
     __shared__ __align__(16) uint16_t lv[2][kChunk * DVB];
     __shared__ __align__(16) uint16_t ls[2][DVB * DK];
@@ -567,68 +609,66 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
     if (!s.open(a)) return;
     const int64_t row0 = s.row0(a.reverse);
     const int rows = static_cast<int>(s.rows), wave = wave_id(), lane = threadIdx.x % kWave, i16 = lane % 16, g = lane / 16;
-    Stage<DK, VEC, 512> sk;
-    Stage<DVB, VEC, 512> sv;
-    sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
-    sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
-    sk.load(rows);
-    sv.load(rows);
-    tab.fill(a.log_decay[s.hv] * 1.4426950408889634f, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
-    auto stage = [&](int c0) {  // chunk c0 from registers to LDS
-        const int b = (c0 / kChunk) & 1;
-        sk.store(lk[b]);
-        sv.store(lv[b]);
-        if (sv.special()) odd_chunk[b] = c0;
-    };
-    auto special = [&](int c0) { return __builtin_amdgcn_readfirstlane(odd_chunk[(c0 / kChunk) & 1]) == c0; };
+    tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
     if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
     __syncthreads();
-    auto ahead = [&](int left) {
-        if (left <= 0) return;
-        sk.load(left);
-        sv.load(left);
-    };
     if (wave < 4) {
-        RowLoads<DK, VEC> q;
+        RowLoads<DK, VEC, 2> q;
         q.open(s.row(a, a.q, row0), a.q, a.reverse, wave, i16, g);
-        q.load(rows);
+        q.template load<0>(rows);
+        q.template load<1>(rows - kChunk);
+        Decays d;
+        d.open(a.log_decay[s.hv], a.alpha, a.beta, a.shift, wave, i16, g);
         Output<DVB> out;
         out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, s.vb * DVB, wave, i16,
                  g);
-        stage(0);
-        ahead(rows - kChunk);
         lds_barrier();
-        for (int c0 = 0; c0 < rows; c0 += kChunk) {
-            const int b = (c0 / kChunk) & 1, left = rows - c0;
-            u32x4 qf[DK / 32];
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk) qf[kk] = q.f[kk];
-            if (left > kChunk) stage(c0 + kChunk);
-            out.flush();
-            ahead(left - 2 * kChunk);
-            if (left > kChunk) q.load(left - kChunk);
+        auto step = [&]<int SET>(Set<SET>, int c0) {
+            const int left = rows - c0;
             f32x4 O[DVB / 16];
-            row_outputs<DK, DVB, false>(lk[b], lv[b], ls[b], tab, qf, wave, lane, special(c0), O);
+            row_outputs<DK, DVB, false>(
+                lk[SET], lv[SET], ls[SET], d, q.f[SET], wave, lane, __builtin_amdgcn_readfirstlane(odd_chunk[SET]) == c0, O,
+                [&] { out.flush(); }, [&] { if (left > 2 * kChunk) q.template load<SET>(left - 2 * kChunk); });
             out.put(O, left < kChunk ? left : kChunk);
             lds_barrier();
+        };
+        for (int c0 = 0; c0 < rows; c0 += 2 * kChunk) {
+            step(Set<0>{}, c0);
+            if (c0 + kChunk < rows) step(Set<1>{}, c0 + kChunk);
         }
         out.flush();
     } else {
         const int w4 = wave - 4;
+        Stage<DK, VEC, 256> sk;
+        Stage<DVB, VEC, 256> sv;
+        sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+        sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
+        sk.load(rows);
+        sv.load(rows);
+        // a chunk to LDS, the one after it to registers
+        auto stage = [&](int c0) {
+            const int b = (c0 / kChunk) & 1;
+            sk.store(lk[b]);
+            sv.store(lv[b]);
+            if (sv.special()) odd_chunk[b] = c0;
+            if (c0 + kChunk >= rows) return;
+            sk.load(rows - c0 - kChunk);
+            sv.load(rows - c0 - kChunk);
+        };
         Wave<DK, NV, DVB> w;
         w.open(a.log_decay[s.hv], a.gamma, a.shift);
         enter(w, a, s, w4, lane);
         stage(0);
-        ahead(rows - kChunk);
         w.publish(ls[0], w4 * NV);
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            if (left > kChunk) stage(c0 + kChunk);
-            ahead(left - 2 * kChunk);
             w.load_values(lv[b], w4 * NV);
-            w.template update<true>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
-            if (left > kChunk) w.publish(ls[b ^ 1], w4 * NV);
+            w.template update<true, PRE>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
+            if (left > kChunk) {
+                stage(c0 + kChunk);
+                w.publish(ls[b ^ 1], w4 * NV);
+            }
             lds_barrier();
         }
         if (s.last && a.fin)
@@ -654,41 +694,21 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
     if (!s.open(a)) return;
     const int64_t row0 = s.row0(a.reverse);
     const int rows = static_cast<int>(s.rows), wave = wave_id(), lane = threadIdx.x % kWave, i16 = lane % 16, g = lane / 16;
-    tab.fill(a.log_decay[s.hv] * 1.4426950408889634f, a.alpha, a.beta, a.gamma, a.shift, threadIdx.x);
+    tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
     if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
     __syncthreads();
     if (wave < 8) {
-        Stage<DK, VEC, 512> sk;
-        Stage<DV, VEC, 512> sv;
-        sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
-        sv.open(s.row(a, a.v, row0), a.v, a.reverse, 0);
-        sk.load(rows);
-        sv.load(rows);
-        auto stage = [&](int c0) {
-            const int b = (c0 / kChunk) & 1;
-            sk.store(lk[b]);
-            sv.store(lv[b]);
-            if (sk.special() || sv.special()) odd_chunk[b] = c0;
-        };
-        auto special = [&](int c0) { return __builtin_amdgcn_readfirstlane(odd_chunk[(c0 / kChunk) & 1]) == c0; };
-        auto ahead = [&](int left) {
-            if (left <= 0) return;
-            sk.load(left);
-            sv.load(left);
-        };
+        Decays d;
+        d.open(a.log_decay[s.hv], a.alpha, a.beta, a.shift, wave % 4, i16, g);
         auto walk = [&](auto& q, auto& out, auto&& outputs) {
             q.load(rows);
-            stage(0);
-            ahead(rows - kChunk);
             lds_barrier();
             for (int c0 = 0; c0 < rows; c0 += kChunk) {
                 const int b = (c0 / kChunk) & 1, left = rows - c0;
                 auto qf = q;
-                if (left > kChunk) stage(c0 + kChunk);
                 out.flush();
-                ahead(left - 2 * kChunk);
                 if (left > kChunk) q.load(left - kChunk);
-                outputs(b, qf.f, left < kChunk ? left : kChunk, special(c0));
+                outputs(b, qf.f[0], left < kChunk ? left : kChunk, __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0);
                 lds_barrier();
             }
             out.flush();
@@ -700,7 +720,7 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, 0, wave, i16, g);
             walk(q, out, [&](int b, const u32x4(&f)[DK / 32], int n, bool odd) {
                 f32x4 O[DV / 16];
-                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], tab, f, wave, lane, odd, O);
+                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], d, f, wave, lane, odd, O, [] {}, [] {});
                 out.put(O, n);
             });
         } else {
@@ -710,21 +730,42 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             out.open(z.o, s.batch(a) * z.o_sb + s.hv * z.o_sh, row0, z.o_st, z.o_f32, z.o_vec, a.reverse, a.k.dim, 0, wave - 4, i16, g);
             walk(q, out, [&](int b, const u32x4(&f)[DV / 32], int n, bool odd) {
                 f32x4 O[DK / 16];
-                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], tab, f, wave - 4, lane, odd, O);
+                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], d, f, wave - 4, lane, odd, O, [] {}, [] {});
                 out.put(O, n);
             });
         }
     } else {
         const int w4 = wave - 8;
+        Stage<DK, VEC, 256> sk;
+        Stage<DV, VEC, 256> sv;
+        sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
+        sv.open(s.row(a, a.v, row0), a.v, a.reverse, 0);
+        auto ahead = [&](int left) {
+            if (left <= 0) return;
+            sk.load(left);
+            sv.load(left);
+        };
+        auto stage = [&](int c0) {
+            const int b = (c0 / kChunk) & 1;
+            sk.store(lk[b]);
+            sv.store(lv[b]);
+            if (sk.special() || sv.special()) odd_chunk[b] = c0;
+        };
+        sk.load(rows);
+        sv.load(rows);
         Wave<DK, NV, DV> w;
         w.open(a.log_decay[s.hv], a.gamma, a.shift);
         enter(w, a, s, w4, lane);
+        stage(0);
+        ahead(rows - kChunk);
         w.publish(ls[0], w4 * NV);
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
+            if (left > kChunk) stage(c0 + kChunk);
+            ahead(left - 2 * kChunk);
             w.load_values(lv[b], w4 * NV);
-            w.template update<true>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
+            w.template update<true, 2>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
             if (left > kChunk) w.publish(ls[b ^ 1], w4 * NV);
             lds_barrier();
         }
@@ -761,7 +802,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
     const int wave = wave_id(), lane = threadIdx.x % kWave;
     Wave<DK, NV, DVB> w;
     w.open(a.log_decay[s.hv], a.gamma, a.shift);
-    tab.fill(w.g2, 0.0f, 0.0f, a.gamma, a.shift, threadIdx.x);
+    tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
     float more = 1.0f;
     for (int c0 = 0; c0 < rows; c0 += kChunk) {
         lds_barrier();
@@ -773,7 +814,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
             sv.load(kChunk);
         }
         w.load_values(lv, wave * NV);
-        w.template update<false>(lk, tab, kChunk, more);
+        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, tab, kChunk, more);
         more *= w.aC;
     }
     float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
