@@ -202,7 +202,6 @@ template <int DK, int NV, int COLSV>
 struct Wave {
     static constexpr int NM = NV / 16, NT = DK / 16;
     f32x4 S[NT][NM];  // S[t][m]: keys 16t + 4g + 0..3 of value channel 16m + i16
-    u32x4 vf[2][NM];  // value channel 16m + i16 of rows 32h + 4g + 0..3 and 32h + 16 + 4g + 0..3
     float g2, aC, gamma;
     int i16, g, shift;
 
@@ -218,13 +217,6 @@ struct Wave {
     }
     // row of element e of a transposed fragment, within its 32 rows
     __device__ __forceinline__ int row_of(int e) const { return 4 * g + (e & 3) + 16 * (e >> 2); }
-
-    __device__ __forceinline__ void load_values(const uint16_t* lv, int col0) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
-    }
 
     // The bf16 copy for the row waves: a row of DK keys for each value channel, from row row0 on.
     __device__ __forceinline__ void publish(uint16_t* ls, int row0) const {
@@ -243,14 +235,20 @@ struct Wave {
     // more. The weighted v is taken as a sum of two bf16 values (the second holds what the first rounds
     // off), so the state keeps about 17 bits of every term.
     template <bool KEEP, int PRE>
-    __device__ __forceinline__ void update(const uint16_t* lk, const Table& tab, int n, float more) {
+    __device__ __forceinline__ void update(const uint16_t* lk, const uint16_t* lv, int col0, const Table& tab, int n, float more) {
         const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
-        // a half's first PRE loads are issued before its values are weighted, the second half's before the
-        // first's products: their latency is behind other work
-        u32x4 kf[2][PRE];
+        // a half's first PRE loads are issued before its values are weighted, the second half's (registers
+        // allowing) before the first's products: their latency is behind other work
+        constexpr bool kBoth = PRE > 2;
+        u32x4 vf[2][NM], kf[2][PRE];
+        auto fetch = [&](int h) {
 #pragma unroll
-        for (int t = 0; t < PRE; ++t) kf[0][t] = columns<DK, false>(lk, t, 0, i16, g);
-        loads_first();
+            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
+#pragma unroll
+            for (int t = 0; t < PRE; ++t) kf[h][t] = columns<DK, false>(lk, t, h, i16, g);
+            loads_first();
+        };
+        fetch(0);
         if constexpr (KEEP) {
             const float an = n == kChunk ? aC : power(g2, n);
 #pragma unroll
@@ -263,6 +261,7 @@ struct Wave {
         u32x4 hi[NM], lo[NM];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !kBoth) fetch(1);
             f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 4 * g),
                            *reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 16 + 4 * g)};
             float w[8];
@@ -287,11 +286,7 @@ struct Wave {
                                            __builtin_amdgcn_fmed3f(u1 - bf16_hi(x), -1e38f, 1e38f));
                 }
             }
-            if (h == 0) {
-#pragma unroll
-                for (int t = 0; t < PRE; ++t) kf[1][t] = columns<DK, false>(lk, t, 1, i16, g);
-                loads_first();
-            }
+            if (h == 0 && kBoth) fetch(1);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const u32x4 k = t < PRE ? kf[h][t < PRE ? t : 0] : columns<DK, false>(lk, t, h, i16, g);
@@ -410,19 +405,22 @@ struct Output {
 
 // Decays of a row wave's scores and of what the state gives, the same for every chunk.
 struct Decays {
-    float score[4][4];  // alpha * a^n for row 16w + i16 and row 16jb + 4g + r, n apart
-    float carry;        // beta * a^(16w + i16 + shift)
+    float near[4], far[4];  // alpha * a^n of the wave's own tile, and of one 16 rows up
+    float down[3];          // a^0, a^16, a^32 by tile, for tiles further up
+    float carry;            // beta * a^(16w + i16 + shift)
     __device__ __forceinline__ void open(float log_decay, float alpha, float beta, int shift, int w, int i16, int g) {
         const float g2 = log_decay * 1.4426950408889634f;
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb)
+        for (int r = 0; r < 4; ++r) {
+            const int n = i16 - 4 * g - r;
+            near[r] = alpha * power(g2, n < 0 ? 0 : n);
+            far[r] = alpha * power(g2, 16 + n);
+        }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = 16 * (w - jb) + i16 - 4 * g - r;
-                score[jb][r] = alpha * power(g2, n < 0 ? 0 : n);
-            }
+        for (int jb = 0; jb < 3; ++jb) down[jb] = power(g2, w > jb ? 16 * (w - jb - 1) : 0);
         carry = beta * power(g2, 16 * w + i16 + shift);
     }
+    __device__ __forceinline__ float score(int jb, int w, int r) const { return jb >= w || jb == 3 ? near[r] : far[r] * down[jb < 3 ? jb : 0]; }
 };
 
 // The outputs of 16 rows of a chunk (rows 16w + i16): O[m] holds value channels 16m + 4g + 0..3.
@@ -453,7 +451,7 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
         float x[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // a later row's product is dropped, whatever it holds
-            x[r] = 16 * (w - jb) + i16 - 4 * g - r >= 0 ? acc[jb][r] * d.score[jb][r] : 0.0f;
+            x[r] = 16 * (w - jb) + i16 - 4 * g - r >= 0 ? acc[jb][r] * d.score(jb, w, r) : 0.0f;
         p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
     first();
@@ -663,8 +661,7 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            w.load_values(lv[b], w4 * NV);
-            w.template update<true, PRE>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
+            w.template update<true, PRE>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk, 1.0f);
             if (left > kChunk) {
                 stage(c0 + kChunk);
                 w.publish(ls[b ^ 1], w4 * NV);
@@ -705,10 +702,7 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             lds_barrier();
             for (int c0 = 0; c0 < rows; c0 += kChunk) {
                 const int b = (c0 / kChunk) & 1, left = rows - c0;
-                auto qf = q;
-                out.flush();
-                if (left > kChunk) q.load(left - kChunk);
-                outputs(b, qf.f[0], left < kChunk ? left : kChunk, __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0);
+                outputs(b, left, __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0);
                 lds_barrier();
             }
             out.flush();
@@ -718,20 +712,22 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             Output<DV> out;
             q.open(s.row(a, a.q, row0), a.q, a.reverse, wave, i16, g);
             out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, 0, wave, i16, g);
-            walk(q, out, [&](int b, const u32x4(&f)[DK / 32], int n, bool odd) {
+            walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DV / 16];
-                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], d, f, wave, lane, odd, O, [] {}, [] {});
-                out.put(O, n);
+                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], d, q.f[0], wave, lane, odd, O, [&] { out.flush(); },
+                                           [&] { if (left > kChunk) q.load(left - kChunk); });
+                out.put(O, left < kChunk ? left : kChunk);
             });
         } else {
             RowLoads<DV, VEC> q;
             Output<DK> out;
             q.open(s.row(a, z.q, row0), z.q, a.reverse, wave - 4, i16, g);
             out.open(z.o, s.batch(a) * z.o_sb + s.hv * z.o_sh, row0, z.o_st, z.o_f32, z.o_vec, a.reverse, a.k.dim, 0, wave - 4, i16, g);
-            walk(q, out, [&](int b, const u32x4(&f)[DV / 32], int n, bool odd) {
+            walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DK / 16];
-                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], d, f, wave - 4, lane, odd, O, [] {}, [] {});
-                out.put(O, n);
+                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], d, q.f[0], wave - 4, lane, odd, O, [&] { out.flush(); },
+                                          [&] { if (left > kChunk) q.load(left - kChunk); });
+                out.put(O, left < kChunk ? left : kChunk);
             });
         }
     } else {
@@ -740,16 +736,14 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         Stage<DV, VEC, 256> sv;
         sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
         sv.open(s.row(a, a.v, row0), a.v, a.reverse, 0);
-        auto ahead = [&](int left) {
-            if (left <= 0) return;
-            sk.load(left);
-            sv.load(left);
-        };
         auto stage = [&](int c0) {
             const int b = (c0 / kChunk) & 1;
             sk.store(lk[b]);
             sv.store(lv[b]);
             if (sk.special() || sv.special()) odd_chunk[b] = c0;
+            if (c0 + kChunk >= rows) return;
+            sk.load(rows - c0 - kChunk);
+            sv.load(rows - c0 - kChunk);
         };
         sk.load(rows);
         sv.load(rows);
@@ -757,16 +751,15 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         w.open(a.log_decay[s.hv], a.gamma, a.shift);
         enter(w, a, s, w4, lane);
         stage(0);
-        ahead(rows - kChunk);
         w.publish(ls[0], w4 * NV);
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            if (left > kChunk) stage(c0 + kChunk);
-            ahead(left - 2 * kChunk);
-            w.load_values(lv[b], w4 * NV);
-            w.template update<true, 2>(lk[b], tab, left < kChunk ? left : kChunk, 1.0f);
-            if (left > kChunk) w.publish(ls[b ^ 1], w4 * NV);
+            w.template update<true, 1>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk, 1.0f);
+            if (left > kChunk) {
+                stage(c0 + kChunk);
+                w.publish(ls[b ^ 1], w4 * NV);
+            }
             lds_barrier();
         }
         if (s.last && a.fin)
@@ -813,8 +806,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
             sk.load(kChunk);
             sv.load(kChunk);
         }
-        w.load_values(lv, wave * NV);
-        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, tab, kChunk, more);
+        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lv, wave * NV, tab, kChunk, more);
         more *= w.aC;
     }
     float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
