@@ -1059,28 +1059,40 @@ def cconv_bwd_ex(x, dy, w, bias=None, *, activation="silu", init_state=None, d_i
 def _heads(t, name: str, shape=None, packed: bool = False) -> Rows:
     """bf16 rows of heads, [B, T, H, D] (packed batches and single tokens: [rows, H, D]) with unit
     channel stride, as the library takes them; `shape`: what it must have."""
-    _dev(t, name)
-    d = 3 if packed else 4
-    if t.dtype != torch.bfloat16 or t.dim() != d or (t.stride(d - 1) != 1 and t.shape[d - 1] > 1):
-        kind = "[rows, H, D]" if packed else "[B, T, H, D]"
-        raise ValueError(f"{name} must be bf16 {kind} with unit channel stride")
+    st = t.stride()
+    # one test on the per-call path; what is wrong is looked up only when it fails
+    if not t.is_cuda or t.get_device() != _current_device() or t.dtype is not torch.bfloat16 or len(st) != 4 - packed or st[-1] != 1:
+        _dev(t, name)
+        if t.dtype is not torch.bfloat16 or len(st) != 4 - packed or t.shape[-1] > 1:
+            kind = "[rows, H, D]" if packed else "[B, T, H, D]"
+            raise ValueError(f"{name} must be bf16 {kind} with unit channel stride")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
-    st = t.stride()
     return Rows(t.data_ptr(), 0, st[0], st[1]) if packed else Rows(t.data_ptr(), st[0], st[1], st[2])
 
 
-def _decay(log_decay, HV: int):
-    _dev(log_decay, "log_decay")
-    if log_decay.dtype != torch.float32 or log_decay.shape != (HV,) or not log_decay.is_contiguous():
-        raise ValueError("log_decay must be a contiguous fp32 [HV] tensor")
+def _plain(t, name: str, kind: str, dtype, shape) -> int:
+    """The address of a contiguous tensor of this dtype and shape on the current device."""
+    if not t.is_cuda or t.get_device() != _current_device():
+        _dev(t, name)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {kind} tensor")
+    return t.data_ptr()
 
 
-def _workspace(t, need: int, dev):
-    """The caller's workspace, or a new one; (tensor or None, bytes)."""
+def _decay(log_decay, HV: int) -> int:
+    return _plain(log_decay, "log_decay", "fp32 [HV]", torch.float32, (HV,))
+
+
+def _workspace(t, need: int, like):
+    """The caller's workspace, or a new one next to `like`; (tensor or None, address, bytes)."""
     if t is None:
-        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
-    return t, _ws(t)
+        if not need:
+            return None, None, 0
+        t = like.new_empty(need, dtype=torch.uint8)
+        return t, t.data_ptr(), need
+    n = _ws(t)
+    return t, t.data_ptr(), n
 
 
 def cconv_linattn_fwd_workspace_bytes(B, T, HV, Dk, Dv, nseq: int = -1) -> int:
@@ -1123,28 +1135,26 @@ def cconv_linattn_fwd(q, k, v, log_decay, *, scale: float = 1.0, init_state=None
     packed = cu_seqlens is not None
     B, T, H, HV, Dk, Dv, n, nseq = _linattn_sizes(q, v, cu_seqlens)
     rq, rk, rv = _heads(q, "q", None, packed), _heads(k, "k", q.shape, packed), _heads(v, "v", q.shape[:-2] + v.shape[-2:], packed)
-    _decay(log_decay, HV)
-    dev = q.device
+    ld = _decay(log_decay, HV)
     _out(init_state, "init_state", (n, HV, Dk, Dv), _F32)
     if final_state is None:
         if want_final_state:
-            final_state = torch.empty((n, HV, Dk, Dv), dtype=torch.float32, device=dev)
+            final_state = log_decay.new_empty((n, HV, Dk, Dv))
     else:
         _out(final_state, "final_state", (n, HV, Dk, Dv), _F32)
     if o is None:
-        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+        o = v.new_empty(v.shape)
     ro = _heads(o, "o", v.shape, packed)
-    if packed:
-        if status is None:
-            status = torch.empty(1, dtype=torch.int32, device=dev)
-        _out(status, "status", (1,), _I32)
-    else:
+    if not packed:
         status = None
+    elif status is None:
+        status = cu_seqlens.new_empty(1)
+    else:
+        _out(status, "status", (1,), _I32)
     L = lib()
-    workspace, ws_bytes = _workspace(workspace, L.cconv_linattn_fwd_workspace_bytes(B, T, nseq, HV, Dk, Dv), dev)
-    _check(L.cconv_linattn_fwd(rq, rk, rv, _ptr(log_decay), scale, _ptr(init_state), ro, _ptr(final_state),
-                               _ptr(cu_seqlens), nseq, _ptr(status), _ptr(workspace), ws_bytes, B, T, H, HV, Dk, Dv,
-                               _stream(stream)), "cconv_linattn_fwd")
+    workspace, ws, ws_bytes = _workspace(workspace, L.cconv_linattn_fwd_workspace_bytes(B, T, nseq, HV, Dk, Dv), q)
+    _check(L.cconv_linattn_fwd(rq, rk, rv, ld, scale, _ptr(init_state), ro, _ptr(final_state), _ptr(cu_seqlens), nseq,
+                               _ptr(status), ws, ws_bytes, B, T, H, HV, Dk, Dv, _stream(stream)), "cconv_linattn_fwd")
     return o, final_state, status
 
 
@@ -1158,32 +1168,31 @@ def cconv_linattn_bwd(q, k, v, log_decay, d_o, *, scale: float = 1.0, init_state
     B, T, H, HV, Dk, Dv, n, nseq = _linattn_sizes(q, v, cu_seqlens)
     rq, rk, rv = _heads(q, "q", None, packed), _heads(k, "k", q.shape, packed), _heads(v, "v", q.shape[:-2] + v.shape[-2:], packed)
     rdo = _heads(d_o, "d_o", v.shape, packed)
-    _decay(log_decay, HV)
-    dev = q.device
+    ld = _decay(log_decay, HV)
     _out(init_state, "init_state", (n, HV, Dk, Dv), _F32)
     _out(d_final_state, "d_final_state", (n, HV, Dk, Dv), _F32)
     if d_init_state is None:
         if want_d_init_state:
-            d_init_state = torch.empty((n, HV, Dk, Dv), dtype=torch.float32, device=dev)
+            d_init_state = log_decay.new_empty((n, HV, Dk, Dv))
     else:
         _out(d_init_state, "d_init_state", (n, HV, Dk, Dv), _F32)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        dq = q.new_empty(q.shape)
     if dk is None:
-        dk = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        dk = q.new_empty(q.shape)
     if dv is None:
-        dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+        dv = v.new_empty(v.shape)
     outs = _heads(dq, "dq", q.shape, packed), _heads(dk, "dk", q.shape, packed), _heads(dv, "dv", v.shape, packed)
-    if packed:
-        if status is None:
-            status = torch.empty(1, dtype=torch.int32, device=dev)
-        _out(status, "status", (1,), _I32)
-    else:
+    if not packed:
         status = None
+    elif status is None:
+        status = cu_seqlens.new_empty(1)
+    else:
+        _out(status, "status", (1,), _I32)
     L = lib()
-    workspace, ws_bytes = _workspace(workspace, L.cconv_linattn_bwd_workspace_bytes(B, T, nseq, H, HV, Dk, Dv), dev)
-    _check(L.cconv_linattn_bwd(rq, rk, rv, _ptr(log_decay), scale, _ptr(init_state), rdo, _ptr(d_final_state), *outs,
-                               _ptr(d_init_state), _ptr(cu_seqlens), nseq, _ptr(status), _ptr(workspace), ws_bytes, B, T,
+    workspace, ws, ws_bytes = _workspace(workspace, L.cconv_linattn_bwd_workspace_bytes(B, T, nseq, H, HV, Dk, Dv), q)
+    _check(L.cconv_linattn_bwd(rq, rk, rv, ld, scale, _ptr(init_state), rdo, _ptr(d_final_state), *outs,
+                               _ptr(d_init_state), _ptr(cu_seqlens), nseq, _ptr(status), ws, ws_bytes, B, T,
                                H, HV, Dk, Dv, _stream(stream)), "cconv_linattn_bwd")
     return dq, dk, dv, d_init_state, status
 
@@ -1200,51 +1209,47 @@ def cconv_linattn_update(q, k, v, log_decay, state, state_indices=None, *, scale
     if v.shape[0] != N:
         raise ValueError("v must have q's rows")
     HV, Dv = v.shape[1:]
-    _decay(log_decay, HV)
-    _dev(state, "state")
-    if state.dtype != torch.float32 or state.dim() != 4 or state.shape[1:] != (HV, Dk, Dv) or not state.is_contiguous():
-        raise ValueError("state must be a contiguous fp32 [S, HV, Dk, Dv] tensor")
+    ld = _decay(log_decay, HV)
+    pool = _plain(state, "state", "fp32 [S, HV, Dk, Dv]", torch.float32, (state.shape[0], HV, Dk, Dv))
     idx = None
     if state_indices is not None:
-        _dev(state_indices, "state_indices")
-        if state_indices.dtype != torch.int32 or state_indices.shape != (N,) or not state_indices.is_contiguous():
-            raise ValueError("state_indices must be a contiguous int32 [N] tensor")
-        idx = state_indices.data_ptr()
+        idx = _plain(state_indices, "state_indices", "int32 [N]", torch.int32, (N,))
     if o is None:
-        o = torch.empty((N, HV, Dv), dtype=torch.bfloat16, device=q.device)
+        o = q.new_empty((N, HV, Dv))
     ro = _heads(o, "o", v.shape, True)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=q.device)
+        status = (q if idx is None else state_indices).new_empty(1, dtype=torch.int32)
     else:
         _out(status, "status", (1,), _I32)
-    _check(lib().cconv_linattn_update(rq, rk, rv, log_decay.data_ptr(), scale, state.data_ptr(), state.shape[0], idx, ro,
-                                      N, H, HV, Dk, Dv, status.data_ptr(), _stream(stream)), "cconv_linattn_update")
+    _check(lib().cconv_linattn_update(rq, rk, rv, ld, scale, pool, state.shape[0], idx, ro, N, H, HV, Dk, Dv,
+                                      status.data_ptr(), _stream(stream)), "cconv_linattn_update")
     return o, status
 
 
 def _norm_side(q, k, wq, wk, table, positions):
-    """The checks that both passes of the norm share: (rows of q, rows of k, weight dtype, P, R)."""
+    """The checks that both passes of the norm share: the arguments up to the positions as the library
+    takes them (positions are not read without a table)."""
     rq, rk = _heads(q, "q"), _heads(k, "k")
-    D = q.shape[3]
-    if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+    B, T, _, D = q.shape
+    ks = k.shape
+    if ks[0] != B or ks[1] != T or ks[3] != D:
         raise ValueError("k must have q's batch, rows and channels")
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        _dev(w, name)
-        if w.dtype not in _WT or w.shape != (D,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 or fp32 [D] tensor")
-    if wq.dtype != wk.dtype:
-        raise ValueError("wq and wk must have one dtype")
+    wdt = wq.dtype
+    if wdt not in _WT:
+        raise ValueError("wq must be a contiguous bf16 or fp32 [D] tensor")
+    pq, pk = _plain(wq, "wq", "bf16 or fp32 [D]", wdt, (D,)), _plain(wk, "wk", "[D] (of wq's dtype)", wdt, (D,))
     P = R = 0
+    pt = pp = None
     if table is not None:
-        _dev(table, "table")
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+        if table.dim() != 2:
             raise ValueError("table must be a contiguous fp32 [P, R] tensor")
         P, R = table.shape
+        pt = _plain(table, "table", "fp32 [P, R]", torch.float32, (P, R))
     if positions is not None:
-        _dev(positions, "positions")
-        if positions.dtype != torch.int32 or positions.shape != q.shape[:2] or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 [B, T] tensor")
-    return rq, rk, (BF16 if wq.dtype == torch.bfloat16 else F32), P, R
+        pp = _plain(positions, "positions", "int32 [B, T]", torch.int32, (B, T))
+    if not R:
+        pt = pp = None
+    return rq, rk, pq, pk, (BF16 if wdt is torch.bfloat16 else F32), pt, P, R, pp
 
 
 def cconv_qknorm_fwd(q, k, wq, wk, table=None, *, positions=None, eps: float = 1e-6, interleaved: bool = False, yq=None,
@@ -1258,23 +1263,24 @@ def cconv_qknorm_fwd(q, k, wq, wk, table=None, *, positions=None, eps: float = 1
     positions and a table, status (a device int32, else None) receives 0, or 8 when a position lies
     outside the table.
     """
-    rq, rk, wdt, P, R = _norm_side(q, k, wq, wk, table, positions)
+    rq, rk, pq, pk, wdt, pt, P, R, pp = _norm_side(q, k, wq, wk, table, positions)
     B, T, Hq, D = q.shape
     if yq is None:
-        yq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        yq = q.new_empty(q.shape)
     if yk is None:
-        yk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+        yk = k.new_empty(k.shape)
     ryq, ryk = _heads(yq, "yq", q.shape), _heads(yk, "yk", k.shape)
-    pos = positions.data_ptr() if positions is not None and R else None
-    if pos is None:
+    ps = None
+    if pp is None:
         status = None
-    elif status is None:
-        status = torch.empty(1, dtype=torch.int32, device=q.device)
     else:
-        _out(status, "status", (1,), _I32)
-    _check(lib().cconv_qknorm_fwd(rq, rk, wq.data_ptr(), wk.data_ptr(), wdt, table.data_ptr() if R else None, P, R,
-                                  int(interleaved), pos, eps, ryq, ryk, B, T, Hq, k.shape[2], D,
-                                  None if status is None else status.data_ptr(), _stream(stream)), "cconv_qknorm_fwd")
+        if status is None:
+            status = positions.new_empty(1)
+        else:
+            _out(status, "status", (1,), _I32)
+        ps = status.data_ptr()
+    _check(lib().cconv_qknorm_fwd(rq, rk, pq, pk, wdt, pt, P, R, interleaved, pp, eps, ryq, ryk, B, T, Hq, k.shape[2], D, ps,
+                                  _stream(stream)), "cconv_qknorm_fwd")
     return yq, yk, status
 
 
@@ -1286,32 +1292,31 @@ def cconv_qknorm_bwd(q, k, dyq, dyk, wq, wk, table=None, *, positions=None, eps:
                      dq=None, dk=None, dwq=None, dwk=None, status=None, workspace=None, stream=None):
     """Gradients of cconv_qknorm_fwd: returns (dq, dk, dwq, dwk, status); dwq and dwk have the
     weights' dtype (sums over all rows and heads in fp32, in a fixed order)."""
-    rq, rk, wdt, P, R = _norm_side(q, k, wq, wk, table, positions)
+    rq, rk, pq, pk, wdt, pt, P, R, pp = _norm_side(q, k, wq, wk, table, positions)
     B, T, Hq, D = q.shape
-    Hk, dev = k.shape[2], q.device
+    Hk = k.shape[2]
     rdyq, rdyk = _heads(dyq, "dyq", q.shape), _heads(dyk, "dyk", k.shape)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        dq = q.new_empty(q.shape)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+        dk = k.new_empty(k.shape)
     if dwq is None:
-        dwq = torch.empty(D, dtype=wq.dtype, device=dev)
+        dwq = wq.new_empty(D)
     if dwk is None:
-        dwk = torch.empty(D, dtype=wk.dtype, device=dev)
-    _out(dwq, "dwq", (D,), (wq.dtype,))
-    _out(dwk, "dwk", (D,), (wk.dtype,))
+        dwk = wk.new_empty(D)
+    pdwq, pdwk = _plain(dwq, "dwq", "[D] (of the weights' dtype)", wq.dtype, (D,)), _plain(dwk, "dwk", "[D] (of the weights' dtype)", wk.dtype, (D,))
     rdq, rdk = _heads(dq, "dq", q.shape), _heads(dk, "dk", k.shape)
-    pos = positions.data_ptr() if positions is not None and R else None
-    if pos is None:
+    ps = None
+    if pp is None:
         status = None
-    elif status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
     else:
-        _out(status, "status", (1,), _I32)
+        if status is None:
+            status = positions.new_empty(1)
+        else:
+            _out(status, "status", (1,), _I32)
+        ps = status.data_ptr()
     L = lib()
-    workspace, ws_bytes = _workspace(workspace, L.cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D), dev)
-    _check(L.cconv_qknorm_bwd(rq, rk, rdyq, rdyk, wq.data_ptr(), wk.data_ptr(), wdt, table.data_ptr() if R else None, P, R,
-                              int(interleaved), pos, eps, rdq, rdk, dwq.data_ptr(), dwk.data_ptr(), _ptr(workspace),
-                              ws_bytes, B, T, Hq, Hk, D, None if status is None else status.data_ptr(), _stream(stream)),
-           "cconv_qknorm_bwd")
+    workspace, ws, ws_bytes = _workspace(workspace, L.cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D), q)
+    _check(L.cconv_qknorm_bwd(rq, rk, rdyq, rdyk, pq, pk, wdt, pt, P, R, interleaved, pp, eps, rdq, rdk, pdwq, pdwk, ws, ws_bytes,
+                              B, T, Hq, Hk, D, ps, _stream(stream)), "cconv_qknorm_bwd")
     return dq, dk, dwq, dwk, status

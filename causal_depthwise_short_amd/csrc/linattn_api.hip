@@ -25,10 +25,15 @@ constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSequences = int64_t(1) << 24;
 constexpr int64_t kMaxDecodeRows = int64_t(1) << 24;
 constexpr int64_t kMaxStepSlots = int64_t(1) << 18;  // the slot check's bits next to the step's own LDS
-// Segments: enough workgroups for two on each of the 256 CUs, each of at least kMinSegment rows (a
-// segment costs one more read of its k and v and two passes over its state).
+// Segments: about one workgroup for each of the 256 CUs (a second one per CU: the walk of a 32768-row
+// prompt of 16 heads 184 -> 207 us, of a training step at [4, 8192, 32 heads, 128] 1097 -> 1162 us, as each
+// segment costs one more read of its k and v and two passes over its state), of at least kMinSegment rows
+// ([3, 1021, 10 heads]: 118 us at 128 or 64 rows, 128 us at 256; 77 rows of 8 heads: 17 us whole, 25 us in two).
 constexpr int64_t kTargetGroups = 256;
-constexpr int64_t kMinSegment = 256;
+constexpr int64_t kMinSegment = 128;
+// The segments' own sums run in two parts each where that leaves too few workgroups: 1097 -> 1045 us for that
+// training step (128 sums), but 184 -> 190 us for the prompt (240 sums).
+constexpr int64_t kFewSums = 192;
 constexpr int64_t kNormWaves = 4096;      // waves a norm wants before a wave takes several heads in turn
 constexpr int64_t kNormBwdBlocks = 1024;  // blocks of the norm's backward, each with one partial of dw
 
@@ -124,8 +129,12 @@ Cut cut_of(int64_t B, int64_t T, int64_t nseq, int64_t groups) {
     const int64_t rows = B * T;
     const int64_t want = std::max<int64_t>(1, kTargetGroups / std::max<int64_t>(1, groups));  // segments in all
     const int64_t each = std::max<int64_t>(kMinSegment, (rows + want - 1) / want);
-    c.sub = each >= 2 * kMinSegment ? 2 : 1;
-    c.seg_rows = (each + c.sub * kChunk - 1) / (c.sub * kChunk) * (c.sub * kChunk);
+    auto rounded = [&](int sub) { return (each + sub * kChunk - 1) / (sub * kChunk) * (sub * kChunk); };
+    const int64_t n = rounded(1);
+    // (packed: about half of the whole segments are a sequence's last)
+    const int64_t sums = nseq < 0 ? B * ((T + n - 1) / n - 1) : T / n / 2;
+    c.sub = sums * groups < kFewSums && each >= 2 * kMinSegment ? 2 : 1;
+    c.seg_rows = rounded(c.sub);
     if (nseq < 0) {
         c.nseq = B;
         c.segs = std::max<int64_t>(1, (T + c.seg_rows - 1) / c.seg_rows);
@@ -581,13 +590,14 @@ cconv_status_t norm_impl(NormCall c, hipStream_t s) {
     a.D = static_cast<int>(c.D), a.R = static_cast<int>(c.R);
     a.eps = c.eps;
     a.B = c.B, a.T = c.T;
-    // one wave per row and side while that fills the chip; fewer heads a wave otherwise
     if (c.R == 0) a.pos = c.pos = nullptr;  // nothing is rotated: positions are not read
     a.status = c.pos ? c.status : nullptr;
-    const int64_t most = std::max(c.Hq, c.Hk), r = static_cast<int64_t>(rows);
-    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(most, kNormWaves / std::max<int64_t>(1, 2 * r)));
-    a.head_chunk = (most + split - 1) / split;
-    a.chunks = (c.Hq + a.head_chunk - 1) / a.head_chunk + (c.Hk + a.head_chunk - 1) / a.head_chunk;
+    // one wave a row (its cosines and sines loaded once for all heads) while that fills the chip; fewer
+    // heads a wave otherwise
+    const int64_t heads = c.Hq + c.Hk, r = static_cast<int64_t>(rows);
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(heads, kNormWaves / std::max<int64_t>(1, r)));
+    a.head_chunk = (heads + split - 1) / split;
+    a.chunks = (heads + a.head_chunk - 1) / a.head_chunk;
     if (static_cast<__int128>(r) * a.chunks / 4 > kMaxGrid) return CCONV_ERR_BAD_SHAPE;
     a.blocks = norm_blocks(c.B, c.T, a.chunks);
     if (!c.pos && c.status && launch_status(c.status, CCONV_OK, s) != hipSuccess) return CCONV_ERR_LAUNCH;

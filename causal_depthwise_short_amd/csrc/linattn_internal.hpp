@@ -133,7 +133,7 @@ struct NormArgs {
     int w_f32, D, R;
     float eps;
     int64_t B, T;
-    int64_t head_chunk, chunks;  // heads (of q, then k) a wave takes, and chunks of a row
+    int64_t head_chunk, chunks;  // heads (of q's and k's together) a wave takes, and such chunks of a row
     const int32_t* status;       // checked before the call's first write
     float* part;                 // backward: [blocks, 2, D]
     int64_t blocks;

@@ -40,7 +40,7 @@ template <int VEC>
 __device__ __forceinline__ void store_state(float* p, const Vec<VEC>& v) {
     if constexpr (VEC == 4) {
         typedef float f4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<f4*>(p) = f4{v.f[0], v.f[1], v.f[2], v.f[3]};
+        __builtin_nontemporal_store(f4{v.f[0], v.f[1], v.f[2], v.f[3]}, reinterpret_cast<f4*>(p));
     } else {
         *p = v.f[0];
     }

@@ -137,26 +137,41 @@ __device__ __forceinline__ void load_weights(const void* w, int w_f32, const Pla
     }
 }
 
-// The sum over the G lanes of a head, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over the G lanes of a head, in every one of them. Up to 16 lanes each step is one addition that
+// reads its neighbour's register (lane ^ 1, lane ^ 2, then the mirrored half and row, whose sums are by then
+// those of lane ^ 4 and lane ^ 8).
 __device__ __forceinline__ float head_sum(float x, int G) {
-    for (int d = 1; d < G; d *= 2) x += __shfl_xor(x, d);
+    if (G >= 2) x = dpp_add<0xb1>(x);   // quad_perm 1 0 3 2
+    if (G >= 4) x = dpp_add<0x4e>(x);   // quad_perm 2 3 0 1
+    if (G >= 8) x = dpp_add<0x141>(x);  // row_half_mirror
+    if (G >= 16) x = dpp_add<0x140>(x); // row_mirror
+    if (G >= 32) x += __shfl_xor(x, 16);
+    if (G >= 64) x += __shfl_xor(x, 32);
     return x;
 }
 
-// What a wave works on: row `row` (of B*T), heads [h0, h1) of q or k.
+// 1 / sqrt(mean + eps): one instruction, accurate to 1 ulp.
+__device__ __forceinline__ float inv_size(float sum, float inv, float eps) {
+    return __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv, eps));
+}
+
+// What a wave works on: row `row` (of B*T), heads [h0, h1) of q's followed by k's.
 struct Item {
     int64_t row;
-    int is_k, h0, h1;
+    int h0, h1;
 };
 
 __device__ __forceinline__ Item item_of(const NormArgs& a, int64_t i) {
     Item t;
-    const int64_t c = i % a.chunks, qc = (a.q.heads + a.head_chunk - 1) / a.head_chunk;
+    const int all = a.q.heads + a.k.heads;
     t.row = i / a.chunks;
-    t.is_k = c >= qc;
-    const int64_t h = (t.is_k ? c - qc : c) * a.head_chunk, heads = t.is_k ? a.k.heads : a.q.heads;
-    t.h0 = static_cast<int>(h);
-    t.h1 = static_cast<int>(h + a.head_chunk < heads ? h + a.head_chunk : heads);
+    t.h0 = static_cast<int>((i - t.row * a.chunks) * a.head_chunk);
+    t.h1 = static_cast<int>(t.h0 + a.head_chunk < all ? t.h0 + a.head_chunk : all);
     return t;
 }
 
@@ -187,7 +202,8 @@ __device__ __forceinline__ void load_angles(const NormArgs& a, int64_t row, int 
 
 }  // namespace
 
-template <int VP, bool INTER, int SL>
+// FULL: every pair is rotated (R = D), so none has to be told apart.
+template <int VP, bool INTER, int SL, bool FULL>
 __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_fwd_kernel(NormArgs a, int G) {
     if (!positions_good(a)) return;
     constexpr int U = VP == 4 ? 4 : 2;  // heads of a lane in flight
@@ -195,61 +211,65 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_fwd_kernel(NormArgs
     const int64_t i = static_cast<int64_t>(blockIdx.x) * (kNormThreads / kWave) + wave_id();
     if (i >= a.B * a.T * a.chunks) return;
     const Item t = item_of(a, i);
-    const HeadRows& h = t.is_k ? a.k : a.q;
-    const int64_t b = t.row / a.T, tt = t.row % a.T;
-    const uint16_t* x = h.x + b * h.sb + tt * h.st;
-    uint16_t* y = h.y + b * h.ysb + tt * h.yst;
-    float w[SL][2][VP], cs[SL][VP], sn[SL][VP];
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-        const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
-        load_weights<VP, INTER>(h.w, a.w_f32, at, w[s]);
-        load_angles<VP>(a, t.row, at.p0, cs[s], sn[s]);
-    }
+    const int64_t b = t.row / a.T, tt = t.row - b * a.T;
     const float inv = 1.0f / static_cast<float>(a.D);
-    for (int h0 = t.h0; h0 < t.h1; h0 += U * hpi) {
-        float v[U][SL][2][VP];
+    float cs[SL][VP], sn[SL][VP];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+    for (int s = 0; s < SL; ++s) load_angles<VP>(a, t.row, (j + s * G) * VP, cs[s], sn[s]);
+    auto side = [&](const HeadRows& h, int first, int end) {
+        if (first >= end) return;
+        const uint16_t* x = h.x + b * h.sb + tt * h.st;
+        uint16_t* y = h.y + b * h.ysb + tt * h.yst;
+        float w[SL][2][VP];
 #pragma unroll
-            for (int s = 0; s < SL; ++s) {
+        for (int s = 0; s < SL; ++s) load_weights<VP, INTER>(h.w, a.w_f32, Place<VP, INTER>((j + s * G) * VP, a.D, a.R), w[s]);
+        for (int h0 = first; h0 < end; h0 += U * hpi) {
+            float v[U][SL][2][VP];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int s = 0; s < SL; ++s) {
+                    const int head = h0 + u * hpi + sub;
+                    const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                    load_pairs<VP, INTER>(x + head * h.sh, at, head < end, v[u][s]);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
                 const int head = h0 + u * hpi + sub;
-                const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
-                load_pairs<VP, INTER>(x + head * h.sh, at, head < t.h1, v[u][s]);
-            }
+                float ss = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int head = h0 + u * hpi + sub;
-            float ss = 0.0f;
+                for (int s = 0; s < SL; ++s)
 #pragma unroll
-            for (int s = 0; s < SL; ++s)
+                    for (int p = 0; p < VP; ++p) {
+                        ss = __builtin_fmaf(v[u][s][0][p], v[u][s][0][p], ss);
+                        ss = __builtin_fmaf(v[u][s][1][p], v[u][s][1][p], ss);
+                    }
+                const float r = inv_size(head_sum(ss, G), inv, a.eps);
 #pragma unroll
-                for (int p = 0; p < VP; ++p) {
-                    ss = __builtin_fmaf(v[u][s][0][p], v[u][s][0][p], ss);
-                    ss = __builtin_fmaf(v[u][s][1][p], v[u][s][1][p], ss);
+                for (int s = 0; s < SL; ++s) {
+                    const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
+                    float o[2][VP];
+#pragma unroll
+                    for (int p = 0; p < VP; ++p) {
+                        const float e = v[u][s][0][p] * r * w[s][0][p], f = v[u][s][1][p] * r * w[s][1][p];
+                        const bool turn = FULL || at.p0 + p < a.R / 2;  // an unrotated channel never meets its neighbour
+                        o[0][p] = turn ? __builtin_fmaf(e, cs[s][p], -(f * sn[s][p])) : e;
+                        o[1][p] = turn ? __builtin_fmaf(f, cs[s][p], e * sn[s][p]) : f;
+                    }
+                    store_pairs<VP, INTER>(y + head * h.ysh, at, head < end, o);
                 }
-            const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(head_sum(ss, G), inv, a.eps));
-#pragma unroll
-            for (int s = 0; s < SL; ++s) {
-                const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
-                float o[2][VP];
-#pragma unroll
-                for (int p = 0; p < VP; ++p) {
-                    const float e = v[u][s][0][p] * r * w[s][0][p], f = v[u][s][1][p] * r * w[s][1][p];
-                    const bool turn = at.p0 + p < a.R / 2;  // an unrotated channel never meets its neighbour
-                    o[0][p] = turn ? __builtin_fmaf(e, cs[s][p], -(f * sn[s][p])) : e;
-                    o[1][p] = turn ? __builtin_fmaf(f, cs[s][p], e * sn[s][p]) : f;
-                }
-                store_pairs<VP, INTER>(y + head * h.ysh, at, head < t.h1, o);
             }
         }
-    }
+    };
+    const int nq = a.q.heads;
+    side(a.q, t.h0, t.h1 < nq ? t.h1 : nq);
+    side(a.k, (t.h0 > nq ? t.h0 : nq) - nq, t.h1 - nq);
 }
 
 // dx = r (w u' - n mean(w u' n)) with n = x r, u' = dy rotated back; dw = sum u' n over all heads
 // and rows: fp32 sums of each lane, then of the wave's heads and the block's waves in a fixed
 // order, one partial per block.
-template <int VP, bool INTER, int SL>
+template <int VP, bool INTER, int SL, bool FULL>
 __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs a, int G) {
     if (!positions_good(a)) return;
     constexpr int U = VP == 4 ? 2 : 1;
@@ -266,19 +286,17 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
             for (int p = 0; p < VP; ++p) dw[m][s][0][p] = dw[m][s][1][p] = 0.0f;
     const float inv = 1.0f / static_cast<float>(a.D);
 
-    auto work = [&](const Item& t, const HeadRows& h, float (&acc)[SL][2][VP]) {
-        const int64_t b = t.row / a.T, tt = t.row % a.T;
+    float cs[SL][VP], sn[SL][VP];
+    auto work = [&](const Item& t, const HeadRows& h, int first, int end, float (&acc)[SL][2][VP]) {
+        if (first >= end) return;
+        const int64_t b = t.row / a.T, tt = t.row - b * a.T;
         const uint16_t* x = h.x + b * h.sb + tt * h.st;
         const uint16_t* dy = h.dy + b * h.dsb + tt * h.dst;
         uint16_t* dx = h.y + b * h.ysb + tt * h.yst;
-        float w[SL][2][VP], cs[SL][VP], sn[SL][VP];
+        float w[SL][2][VP];
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
-            const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
-            load_weights<VP, INTER>(h.w, a.w_f32, at, w[s]);
-            load_angles<VP>(a, t.row, at.p0, cs[s], sn[s]);
-        }
-        for (int h0 = t.h0; h0 < t.h1; h0 += U * hpi) {
+        for (int s = 0; s < SL; ++s) load_weights<VP, INTER>(h.w, a.w_f32, Place<VP, INTER>((j + s * G) * VP, a.D, a.R), w[s]);
+        for (int h0 = first; h0 < end; h0 += U * hpi) {
             float v[U][SL][2][VP], d[U][SL][2][VP];
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -286,8 +304,8 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
                 for (int s = 0; s < SL; ++s) {
                     const int head = h0 + u * hpi + sub;
                     const Place<VP, INTER> at((j + s * G) * VP, a.D, a.R);
-                    load_pairs<VP, INTER>(x + head * h.sh, at, head < t.h1, v[u][s]);
-                    load_pairs<VP, INTER>(dy + head * h.dsh, at, head < t.h1, d[u][s]);
+                    load_pairs<VP, INTER>(x + head * h.sh, at, head < end, v[u][s]);
+                    load_pairs<VP, INTER>(dy + head * h.dsh, at, head < end, d[u][s]);
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -300,7 +318,7 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
                         ss = __builtin_fmaf(v[u][s][0][p], v[u][s][0][p], ss);
                         ss = __builtin_fmaf(v[u][s][1][p], v[u][s][1][p], ss);
                     }
-                const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(head_sum(ss, G), inv, a.eps));
+                const float r = inv_size(head_sum(ss, G), inv, a.eps);
                 float along = 0.0f;
 #pragma unroll
                 for (int s = 0; s < SL; ++s) {
@@ -308,11 +326,11 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
 #pragma unroll
                     for (int p = 0; p < VP; ++p) {
                         const float e = d[u][s][0][p], f = d[u][s][1][p];
-                        const bool turn = at.p0 + p < a.R / 2;
+                        const bool turn = FULL || at.p0 + p < a.R / 2;
                         const float ue = turn ? __builtin_fmaf(e, cs[s][p], f * sn[s][p]) : e;
                         const float uf = turn ? __builtin_fmaf(f, cs[s][p], -(e * sn[s][p])) : f;
                         const float ne = v[u][s][0][p] * r, nf = v[u][s][1][p] * r;
-                        if (head < t.h1) {  // (absent lanes hold zeros, and r of a zero head may be infinite)
+                        if (head < end) {  // (absent lanes hold zeros, and r of a zero head may be infinite)
                             acc[s][0][p] = __builtin_fmaf(ue, ne, acc[s][0][p]);
                             acc[s][1][p] = __builtin_fmaf(uf, nf, acc[s][1][p]);
                         }
@@ -332,7 +350,7 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
                         o[0][p] = r * __builtin_fmaf(-v[u][s][0][p], m, d[u][s][0][p]);
                         o[1][p] = r * __builtin_fmaf(-v[u][s][1][p], m, d[u][s][1][p]);
                     }
-                    store_pairs<VP, INTER>(dx + head * h.ysh, at, head < t.h1, o);
+                    store_pairs<VP, INTER>(dx + head * h.ysh, at, head < end, o);
                 }
             }
         }
@@ -340,10 +358,11 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWaves;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWaves + wave_id(); i < items; i += stride) {
         const Item t = item_of(a, i);
-        if (t.is_k)
-            work(t, a.k, dw[1]);
-        else
-            work(t, a.q, dw[0]);
+        const int nq = a.q.heads;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) load_angles<VP>(a, t.row, (j + s * G) * VP, cs[s], sn[s]);
+        work(t, a.q, t.h0, t.h1 < nq ? t.h1 : nq, dw[0]);
+        work(t, a.k, (t.h0 > nq ? t.h0 : nq) - nq, t.h1 - nq, dw[1]);
     }
     // the wave's lane groups, then the block's waves
 #pragma unroll
@@ -371,19 +390,30 @@ __global__ __launch_bounds__(kNormThreads) void cconv_qknorm_bwd_kernel(NormArgs
     }
 }
 
-// dw of q and k: a block per 16 columns, 16 threads a column.
-__global__ __launch_bounds__(256) void cconv_qknorm_dw_kernel(const float* part, int64_t blocks, int D, void* dwq,
-                                                              void* dwk, int w_f32, const int32_t* status) {
+// dw of q and k: a block per 16 columns, 64 threads a column, each over its blocks' partials in order.
+__global__ __launch_bounds__(1024) void cconv_qknorm_dw_kernel(const float* part, int64_t blocks, int D, void* dwq,
+                                                               void* dwk, int w_f32, const int32_t* status) {
     if (status && *status != CCONV_OK) return;
-    __shared__ float sums[16][17];
+    __shared__ float sums[64][17];
     const int c = threadIdx.x % 16, r = threadIdx.x / 16, e = blockIdx.x * 16 + c;
     float x = 0.0f;
+    constexpr int kAhead = 8;  // loads in flight
     if (e < 2 * D)
-        for (int64_t b = r; b < blocks; b += 16) x += part[b * 2 * D + e];
+        for (int64_t b = r; b < blocks; b += 64 * kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) v[k] = b + 64 * k < blocks ? part[(b + 64 * k) * 2 * D + e] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x += v[k];
+        }
     sums[r][c] = x;
     __syncthreads();
+    for (int n = 32; n > 0; n /= 2) {
+        if (r < n) sums[r][c] += sums[r + n][c];
+        __syncthreads();
+    }
     if (r == 0 && e < 2 * D) {
-        for (int k = 1; k < 16; ++k) x += sums[k][c];
+        x = sums[0][c];
         void* o = e < D ? dwq : dwk;
         const int at = e < D ? e : e - D;
         if (w_f32)
@@ -421,18 +451,26 @@ static int lanes_of(int D, int R, int vec, bool inter) {
     return G;
 }
 
-template <bool BWD, int VP, bool INTER, int SL>
-static hipError_t norm_go(const NormArgs& a, hipStream_t s) {
+template <bool BWD, int VP, bool INTER, int SL, bool FULL>
+static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
     const int G = lanes_of(a.D, a.R, VP, INTER);
     if constexpr (BWD) {
-        hipLaunchKernelGGL((cconv_qknorm_bwd_kernel<VP, INTER, SL>), dim3(static_cast<uint32_t>(a.blocks)), dim3(kNormThreads),
-                           0, s, a, G);
+        hipLaunchKernelGGL((cconv_qknorm_bwd_kernel<VP, INTER, SL, FULL>), dim3(static_cast<uint32_t>(a.blocks)),
+                           dim3(kNormThreads), 0, s, a, G);
     } else {
         const int64_t waves = a.B * a.T * a.chunks, blocks = (waves + 3) / 4;
-        hipLaunchKernelGGL((cconv_qknorm_fwd_kernel<VP, INTER, SL>), dim3(static_cast<uint32_t>(blocks)), dim3(kNormThreads), 0,
-                           s, a, G);
+        hipLaunchKernelGGL((cconv_qknorm_fwd_kernel<VP, INTER, SL, FULL>), dim3(static_cast<uint32_t>(blocks)),
+                           dim3(kNormThreads), 0, s, a, G);
     }
     return hipGetLastError();
+}
+
+template <bool BWD, int VP, bool INTER, int SL>
+static hipError_t norm_go(const NormArgs& a, hipStream_t s) {
+    if constexpr (VP == 4) {
+        if (a.R == a.D) return norm_launch<BWD, VP, INTER, SL, true>(a, s);
+    }
+    return norm_launch<BWD, VP, INTER, SL, false>(a, s);
 }
 
 template <bool BWD>
@@ -447,7 +485,7 @@ hipError_t launch_qknorm_bwd(const NormArgs& a, int vec, bool inter, hipStream_t
 
 hipError_t launch_qknorm_dw(const float* part, int64_t blocks, int D, void* dwq, void* dwk, int w_f32,
                             const int32_t* status, hipStream_t s) {
-    hipLaunchKernelGGL(cconv_qknorm_dw_kernel, dim3((2 * D + 15) / 16), dim3(256), 0, s, part, blocks, D, dwq, dwk, w_f32,
+    hipLaunchKernelGGL(cconv_qknorm_dw_kernel, dim3((2 * D + 15) / 16), dim3(1024), 0, s, part, blocks, D, dwq, dwk, w_f32,
                        status);
     return hipGetLastError();
 }
