@@ -28,7 +28,7 @@ __device__ __forceinline__ Vec<VEC> load_state(const float* p) {
     Vec<VEC> v;
     if constexpr (VEC == 4) {
         typedef float f4 __attribute__((ext_vector_type(4)));
-        const f4 x = *reinterpret_cast<const f4*>(p);
+        const f4 x = __builtin_nontemporal_load(reinterpret_cast<const f4*>(p));
         v.f[0] = x.x, v.f[1] = x.y, v.f[2] = x.z, v.f[3] = x.w;
     } else {
         v.f[0] = *p;

@@ -51,11 +51,11 @@ struct Place {
 template <int N>
 __device__ __forceinline__ void load_n(const uint16_t* p, float (&f)[N]) {
     if constexpr (N == 8) {
-        const u32x4a v = *reinterpret_cast<const u32x4a*>(p);
+        const u32x4a v = __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(p));
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
     } else if constexpr (N == 4) {
-        const u32x2a v = *reinterpret_cast<const u32x2a*>(p);
+        const u32x2a v = __builtin_nontemporal_load(reinterpret_cast<const u32x2a*>(p));
         f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     } else if constexpr (N == 2) {
         const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
@@ -71,11 +71,11 @@ __device__ __forceinline__ void store_n(uint16_t* p, const float (&f)[N]) {
         u32x4a v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        *reinterpret_cast<u32x4a*>(p) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4a*>(p));
     } else if constexpr (N == 4) {
         u32x2a v;
         v.x = pack_bf16x2(f[0], f[1]), v.y = pack_bf16x2(f[2], f[3]);
-        *reinterpret_cast<u32x2a*>(p) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x2a*>(p));
     } else if constexpr (N == 2) {
         *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
     } else {
