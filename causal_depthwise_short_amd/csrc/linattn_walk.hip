@@ -86,7 +86,7 @@ __device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, i
 
 // `sum`, or NaN where one of the two bf16 values is infinite or NaN.
 __device__ __forceinline__ float nan_if_special(uint32_t pair, float sum) {
-    return __builtin_fmaf(bf16_lo(pair), 0.0f, __builtin_fmaf(bf16_hi(pair), 0.0f, sum));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), bf16x2{}, sum, false);
 }
 
 // LDS tiles have rows of COLS bf16 channels without padding; the 16-byte chunk c of row r lies at place
@@ -181,8 +181,8 @@ __device__ __forceinline__ u32x4 columns(const uint16_t* tile, int x, int h, int
 
 // The same value, unknown to the compiler: what is computed from it is computed in place. (LDS addresses
 // kept from chunk to chunk cost the walks registers that they had to spill.)
-__device__ __forceinline__ int anew(int x) {
-    asm volatile("" : "+v"(x));
+__device__ __forceinline__ int anew(int x, bool on = true) {
+    if (on) asm volatile("" : "+v"(x));
     return x;
 }
 
@@ -198,7 +198,7 @@ struct Table {
 };
 
 // A state wave: a state of DK keys by NV value channels in fp32, and its update by a chunk.
-template <int DK, int NV, int COLSV>
+template <int DK, int NV, int COLSV, bool LEAN = false>
 struct Wave {
     static constexpr int NM = NV / 16, NT = DK / 16;
     f32x4 S[NT][NM];  // S[t][m]: keys 16t + 4g + 0..3 of value channel 16m + i16
@@ -220,7 +220,7 @@ struct Wave {
 
     // The bf16 copy for the row waves: a row of DK keys for each value channel, from row row0 on.
     __device__ __forceinline__ void publish(uint16_t* ls, int row0) const {
-        const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
+        const int lane = anew(threadIdx.x % kWave, LEAN), i16 = lane % 16, g = lane / 16;
         uint16_t* p = ls + (row0 + i16) * DK + 4 * (g % 2);
         const int sw = swizzle<DK>(i16);
 #pragma unroll
@@ -235,8 +235,9 @@ struct Wave {
     // more. The weighted v is taken as a sum of two bf16 values (the second holds what the first rounds
     // off), so the state keeps about 17 bits of every term.
     template <bool KEEP, int PRE>
-    __device__ __forceinline__ void update(const uint16_t* lk, const uint16_t* lv, int col0, const Table& tab, int n, float more) {
-        const int lane = anew(threadIdx.x % kWave), i16 = lane % 16, g = lane / 16;
+    __device__ __forceinline__ void update(const uint16_t* lk, const uint16_t* lv, int col0, const Table& tab, int n, bool special,
+                                           float more) {
+        const int lane = anew(threadIdx.x % kWave, LEAN), i16 = lane % 16, g = lane / 16;
         // a half's first PRE loads are issued before its values are weighted, the second half's (registers
         // allowing) before the first's products: their latency is behind other work
         constexpr bool kBoth = PRE > 2;
@@ -274,18 +275,21 @@ struct Wave {
                     w[e] = gamma * power(g2, left < 0 ? 0 : left) * more;
                 }
             }
+            auto split = [&](auto&& rest) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
+                for (int m = 0; m < NM; ++m)
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const float u0 = bf16_lo(vf[h][m][d]) * w[2 * d], u1 = bf16_hi(vf[h][m][d]) * w[2 * d + 1];
-                    const uint32_t x = pack_bf16x2(u0, u1);
-                    hi[m][d] = x;
-                    // of an infinite or NaN value the rest is made finite: the first part carries it
-                    lo[m][d] = pack_bf16x2(__builtin_amdgcn_fmed3f(u0 - bf16_lo(x), -1e38f, 1e38f),
-                                           __builtin_amdgcn_fmed3f(u1 - bf16_hi(x), -1e38f, 1e38f));
-                }
-            }
+                    for (int d = 0; d < 4; ++d) {
+                        const float u0 = bf16_lo(vf[h][m][d]) * w[2 * d], u1 = bf16_hi(vf[h][m][d]) * w[2 * d + 1];
+                        const uint32_t x = pack_bf16x2(u0, u1);
+                        hi[m][d] = x;
+                        lo[m][d] = pack_bf16x2(rest(u0 - bf16_lo(x)), rest(u1 - bf16_hi(x)));
+                    }
+            };
+            if (!LEAN && __builtin_expect(!special, 1))
+                split([](float x) { return x; });
+            else  // of an infinite or NaN value the rest is made finite: the first part carries it
+                split([](float x) { return __builtin_amdgcn_fmed3f(x, -1e38f, 1e38f); });
             if (h == 0 && kBoth) fetch(1);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -321,7 +325,7 @@ struct RowLoads {
                                           : static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * st + 32 * kk + 8 * g) * 2);
     }
     template <int SET = 0>
-    __device__ __forceinline__ void load(int n) {
+    __device__ __forceinline__ void load(int n) {  // (n <= 0: nothing is read)
         const __amdgpu_buffer_rsrc_t b = chunk_rsrc(p);
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) f[SET][kk] = load8<VEC>(b, row < n ? off[kk] : kNowhere, 0, have - 32 * kk);
@@ -426,13 +430,15 @@ struct Decays {
 // The outputs of 16 rows of a chunk (rows 16w + i16): O[m] holds value channels 16m + 4g + 0..3.
 //   lk, lv  the chunk's keys and values; ls the state's copy, a row of DK keys for each value channel, or,
 //           with FLIP, a row of DV value channels for each key
-//   first, second  what the wave has to issue besides, put between the products
-template <int DK, int DV, bool FLIP, class First, class Second>
+//   between  the next rows' loads, put between the products. Neither they nor anything else branches between
+//            a product and the first use of its result: the compiler has left out the wait states that gfx950
+//            needs there when a branch lay between (seen as one wrong value in four, in the last rows of a segment).
+template <int DK, int DV, bool FLIP, bool LEAN, class Between>
 __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* lv, const uint16_t* ls, const Decays& d,
                                             const u32x4 (&qf)[DK / 32], int w, int lane, bool special,
-                                            f32x4 (&O)[DV / 16], First&& first, Second&& second) {
+                                            f32x4 (&O)[DV / 16], Between&& between) {
     constexpr int NK = DK / 32, NM = DV / 16;
-    lane = anew(lane);
+    lane = anew(lane, LEAN);
     const int i16 = lane % 16, g = lane / 16;
     const int sw = swizzle<DK>(i16);
     // p^T = k q^T with its decays: p[jb] holds rows 16jb + 4g + 0..3 of row 16w + i16. All four tiles, also
@@ -454,7 +460,6 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
             x[r] = 16 * (w - jb) + i16 - 4 * g - r >= 0 ? acc[jb][r] * d.score(jb, w, r) : 0.0f;
         p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
-    first();
     // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (a relative 2^-9 of each
     // entry, as the products' other operand has; the state itself stays in 32 bits).
 #pragma unroll
@@ -472,7 +477,7 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[m][r] = at[r] * d.carry;
     }
-    second();
+    between();
     // o^T += v^T p^T. Where the chunk's values hold infinities or NaN, later rows are left out one by one:
     // they would meet p's zeros and make NaN of rows that do not depend on them.
     if (__builtin_expect(!special, 1)) {
@@ -540,8 +545,8 @@ struct Segment {
 };
 
 // Entries (dk, dv) of a head's matrix: a wave's state from it (added, weighted) and to it.
-template <int DK, int NV, int COLSV>
-__device__ __forceinline__ void add_matrix(Wave<DK, NV, COLSV>& w, const float* m0, float weight, int Dk, int Dv, int dv0, int sk,
+template <int DK, int NV, int COLSV, bool LEAN>
+__device__ __forceinline__ void add_matrix(Wave<DK, NV, COLSV, LEAN>& w, const float* m0, float weight, int Dk, int Dv, int dv0, int sk,
                                            int sv) {
     const __amdgpu_buffer_rsrc_t b = chunk_rsrc(m0);
 #pragma unroll
@@ -556,8 +561,8 @@ __device__ __forceinline__ void add_matrix(Wave<DK, NV, COLSV>& w, const float* 
             }
 }
 
-template <int DK, int NV, int COLSV>
-__device__ __forceinline__ void store_matrix(const Wave<DK, NV, COLSV>& w, float* m0, int Dk, int Dv, int dv0, int sk, int sv) {
+template <int DK, int NV, int COLSV, bool LEAN>
+__device__ __forceinline__ void store_matrix(const Wave<DK, NV, COLSV, LEAN>& w, float* m0, int Dk, int Dv, int dv0, int sk, int sv) {
     const __amdgpu_buffer_rsrc_t b = chunk_rsrc(m0);
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t)
@@ -574,8 +579,8 @@ __device__ __forceinline__ void store_matrix(const Wave<DK, NV, COLSV>& w, float
 }  // namespace
 
 // The state that enters a segment.
-template <int DK, int NV, int COLSV>
-__device__ __forceinline__ void enter(Wave<DK, NV, COLSV>& w, const WalkArgs& a, const Segment& s, int wave, int lane) {
+template <int DK, int NV, int COLSV, bool LEAN>
+__device__ __forceinline__ void enter(Wave<DK, NV, COLSV, LEAN>& w, const WalkArgs& a, const Segment& s, int wave, int lane) {
     constexpr int NT = DK / 16, NM = NV / 16;
     if (s.first > 0) {
         const float* c = a.states + ((s.seg - 1) * a.sub * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * 4 * NV +
@@ -624,9 +629,10 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         auto step = [&]<int SET>(Set<SET>, int c0) {
             const int left = rows - c0;
             f32x4 O[DVB / 16];
-            row_outputs<DK, DVB, false>(
-                lk[SET], lv[SET], ls[SET], d, q.f[SET], wave, lane, __builtin_amdgcn_readfirstlane(odd_chunk[SET]) == c0, O,
-                [&] { out.flush(); }, [&] { if (left > 2 * kChunk) q.template load<SET>(left - 2 * kChunk); });
+            out.flush();
+            row_outputs<DK, DVB, false, DK == 256>(lk[SET], lv[SET], ls[SET], d, q.f[SET], wave, lane,
+                                                   __builtin_amdgcn_readfirstlane(odd_chunk[SET]) == c0, O,
+                                                   [&] { q.template load<SET>(left - 2 * kChunk); });
             out.put(O, left < kChunk ? left : kChunk);
             lds_barrier();
         };
@@ -653,7 +659,7 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
             sk.load(rows - c0 - kChunk);
             sv.load(rows - c0 - kChunk);
         };
-        Wave<DK, NV, DVB> w;
+        Wave<DK, NV, DVB, DK == 256> w;
         w.open(a.log_decay[s.hv], a.gamma, a.shift);
         enter(w, a, s, w4, lane);
         stage(0);
@@ -661,7 +667,8 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            w.template update<true, PRE>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk, 1.0f);
+            w.template update<true, PRE>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
+                                           __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0, 1.0f);
             if (left > kChunk) {
                 stage(c0 + kChunk);
                 w.publish(ls[b ^ 1], w4 * NV);
@@ -714,8 +721,9 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, 0, wave, i16, g);
             walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DV / 16];
-                row_outputs<DK, DV, false>(lk[b], lv[b], ls[b], d, q.f[0], wave, lane, odd, O, [&] { out.flush(); },
-                                           [&] { if (left > kChunk) q.load(left - kChunk); });
+                out.flush();
+                row_outputs<DK, DV, false, true>(lk[b], lv[b], ls[b], d, q.f[0], wave, lane, odd, O,
+                                                 [&] { q.load(left - kChunk); });
                 out.put(O, left < kChunk ? left : kChunk);
             });
         } else {
@@ -725,8 +733,9 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
             out.open(z.o, s.batch(a) * z.o_sb + s.hv * z.o_sh, row0, z.o_st, z.o_f32, z.o_vec, a.reverse, a.k.dim, 0, wave - 4, i16, g);
             walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DK / 16];
-                row_outputs<DV, DK, true>(lv[b], lk[b], ls[b], d, q.f[0], wave - 4, lane, odd, O, [&] { out.flush(); },
-                                          [&] { if (left > kChunk) q.load(left - kChunk); });
+                out.flush();
+                row_outputs<DV, DK, true, true>(lv[b], lk[b], ls[b], d, q.f[0], wave - 4, lane, odd, O,
+                                                [&] { q.load(left - kChunk); });
                 out.put(O, left < kChunk ? left : kChunk);
             });
         }
@@ -747,7 +756,7 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         };
         sk.load(rows);
         sv.load(rows);
-        Wave<DK, NV, DV> w;
+        Wave<DK, NV, DV, true> w;
         w.open(a.log_decay[s.hv], a.gamma, a.shift);
         enter(w, a, s, w4, lane);
         stage(0);
@@ -755,7 +764,8 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            w.template update<true, 1>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk, 1.0f);
+            w.template update<true, 1>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
+                                           __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0, 1.0f);
             if (left > kChunk) {
                 stage(c0 + kChunk);
                 w.publish(ls[b ^ 1], w4 * NV);
@@ -778,6 +788,7 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
     __shared__ __align__(16) uint16_t lk[kChunk * DK];
     __shared__ __align__(16) uint16_t lv[kChunk * DVB];
     __shared__ Table tab;
+    __shared__ int odd_chunk;  // the chunk whose values hold an infinity or NaN
 
     if (a.status && *a.status != CCONV_OK) return;
     Segment s;
@@ -796,17 +807,20 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
     Wave<DK, NV, DVB> w;
     w.open(a.log_decay[s.hv], a.gamma, a.shift);
     tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
+    if (threadIdx.x == 0) odd_chunk = -1;
     float more = 1.0f;
     for (int c0 = 0; c0 < rows; c0 += kChunk) {
         lds_barrier();
         sk.store(lk);
         sv.store(lv);
+        if (sv.special()) odd_chunk = c0;
         lds_barrier();
         if (rows - c0 > kChunk) {
             sk.load(kChunk);
             sv.load(kChunk);
         }
-        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lv, wave * NV, tab, kChunk, more);
+        const bool sv_special = __builtin_amdgcn_readfirstlane(odd_chunk) == c0;
+        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lv, wave * NV, tab, kChunk, sv_special, more);
         more *= w.aC;
     }
     float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
