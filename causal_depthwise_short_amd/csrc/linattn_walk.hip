@@ -337,34 +337,37 @@ struct RowLoads {
 // whose channels go out four at a time are kept packed and stored one chunk late, before the next loads
 // are issued: stores count with the loads that a wave waits for, so a store issued after them would be
 // waited for with them.
-template <int DV>
+//   WIDE  bf16 rows of 16-byte aligned groups of eight channels, without branches; otherwise any rows
+template <int DV, bool WIDE>
 struct Output {
     static constexpr int NM = DV / 16;
-    char* p;
+    char* p;  // lowest row of the chunk that is held, or was last put
     int64_t step;
     u32x2 held[NM];
     int held_rows;
     uint32_t off;
-    int es, vec, left, row, g;  // left: channels from the lane's first on
+    int es, vec, left, row;  // left: channels from the lane's first on
     bool f32;
 
     __device__ __forceinline__ void open(void* o, int64_t head_off, int64_t row0, int64_t o_st, int o_f32, int o_vec, bool reverse,
-                                         int dim, int dv0, int w, int i16, int g_) {
-        f32 = o_f32, es = f32 ? 4 : 2, vec = o_vec, g = g_, row = 16 * w + i16;
+                                         int dim, int dv0, int w, int i16, int g) {
+        f32 = !WIDE && o_f32, es = f32 ? 4 : 2, vec = o_vec, row = 16 * w + i16;
         // pairs of tiles go out eight channels a lane: lane group g then has channels 16 (g % 2) + 8 (g / 2) ..
-        const int c = vec == 8 && !f32 ? 16 * (g % 2) + 8 * (g / 2) : 4 * g;
+        const int c = WIDE ? 16 * (g % 2) + 8 * (g / 2) : 4 * g;
         left = dim - dv0 - c;
-        p = static_cast<char*>(o) + (head_off + (reverse ? row0 - (kChunk - 1) : row0) * o_st) * es;
         step = (reverse ? -kChunk : kChunk) * o_st * es;
+        p = static_cast<char*>(o) + (head_off + (reverse ? row0 - (kChunk - 1) : row0) * o_st) * es - step;
         held_rows = 0;
         off = static_cast<uint32_t>(((reverse ? kChunk - 1 - row : row) * static_cast<int>(o_st) + dv0 + c) * es);
+        if constexpr (WIDE)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) held[m] = u32x2{0u, 0u};
     }
     __device__ __forceinline__ void flush() {
-        if (held_rows == 0) return;
+        if (!WIDE && held_rows == 0) return;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
-        p += step;
         const uint32_t at = row < held_rows ? off : kNowhere;
-        if (vec == 8) {
+        if constexpr (WIDE) {
 #pragma unroll
             for (int m = 0; m < NM; m += 2) {
                 // rows of 16 lanes: the second of the first tile's against the first of the second's, and so on
@@ -383,10 +386,10 @@ struct Output {
 #pragma unroll
         for (int m = 0; m < NM; ++m) held[m] = u32x2{pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3])};
         held_rows = n;
-        if (vec >= 4 && !f32) return;
+        p += step;
+        if (WIDE || (vec >= 4 && !f32)) return;
         held_rows = 0;
         const __amdgpu_buffer_rsrc_t ob = chunk_rsrc(p);
-        p += step;
         const bool in = row < n;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
@@ -430,13 +433,13 @@ struct Decays {
 // The outputs of 16 rows of a chunk (rows 16w + i16): O[m] holds value channels 16m + 4g + 0..3.
 //   lk, lv  the chunk's keys and values; ls the state's copy, a row of DK keys for each value channel, or,
 //           with FLIP, a row of DV value channels for each key
-//   between  the next rows' loads, put between the products. Neither they nor anything else branches between
+//   stores, between  the last chunk's stores and the next rows' loads, put between the products. Neither they nor anything else branches between
 //            a product and the first use of its result: the compiler has left out the wait states that gfx950
 //            needs there when a branch lay between (seen as one wrong value in four, in the last rows of a segment).
-template <int DK, int DV, bool FLIP, bool LEAN, class Between>
+template <int DK, int DV, bool FLIP, bool LEAN, class Stores, class Between>
 __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* lv, const uint16_t* ls, const Decays& d,
                                             const u32x4 (&qf)[DK / 32], int w, int lane, bool special,
-                                            f32x4 (&O)[DV / 16], Between&& between) {
+                                            f32x4 (&O)[DV / 16], Stores&& stores, Between&& between) {
     constexpr int NK = DK / 32, NM = DV / 16;
     lane = anew(lane, LEAN);
     const int i16 = lane % 16, g = lane / 16;
@@ -460,6 +463,7 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
             x[r] = 16 * (w - jb) + i16 - 4 * g - r >= 0 ? acc[jb][r] * d.score(jb, w, r) : 0.0f;
         p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
+    stores();
     // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (a relative 2^-9 of each
     // entry, as the products' other operand has; the state itself stays in 32 bits).
 #pragma unroll
@@ -597,7 +601,7 @@ __device__ __forceinline__ void enter(Wave<DK, NV, COLSV, LEAN>& w, const WalkAr
 
 // The walk: four row waves, then four state waves, of NV value channels each, which also stage the chunks
 // (the row waves' part is the longer).
-template <int DK, int NV, int VEC>
+template <int DK, int NV, int VEC, bool WIDE>
 __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV;
     constexpr int PRE = DK == 256 ? 4 : DK / 16;  // as the registers allow
@@ -622,16 +626,19 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         q.template load<1>(rows - kChunk);
         Decays d;
         d.open(a.log_decay[s.hv], a.alpha, a.beta, a.shift, wave, i16, g);
-        Output<DVB> out;
+        Output<DVB, WIDE> out;
         out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, s.vb * DVB, wave, i16,
                  g);
         lds_barrier();
         auto step = [&]<int SET>(Set<SET>, int c0) {
             const int left = rows - c0;
             f32x4 O[DVB / 16];
-            out.flush();
+            auto late = [&] {
+                if constexpr (WIDE) out.flush();
+            };
+            if constexpr (!WIDE) out.flush();
             row_outputs<DK, DVB, false, DK == 256>(lk[SET], lv[SET], ls[SET], d, q.f[SET], wave, lane,
-                                                   __builtin_amdgcn_readfirstlane(odd_chunk[SET]) == c0, O,
+                                                   __builtin_amdgcn_readfirstlane(odd_chunk[SET]) == c0, O, late,
                                                    [&] { q.template load<SET>(left - 2 * kChunk); });
             out.put(O, left < kChunk ? left : kChunk);
             lds_barrier();
@@ -684,7 +691,7 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 // Two walks over the same rows whose states are each other's transposes: dv (rows k, keys q, values do)
 // and dk (rows v, keys do, values q). One set of state waves serves both, the second set of row waves
 // reading the state's copy by columns; q and do are staged once.
-template <int DK, int DV, int VEC>
+template <int DK, int DV, int VEC, bool WIDE>
 __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a, SecondWalk z) {
     constexpr int NV = DV / 4;
     __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
@@ -716,25 +723,31 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         };
         if (wave < 4) {
             RowLoads<DK, VEC> q;
-            Output<DV> out;
+            Output<DV, WIDE> out;
             q.open(s.row(a, a.q, row0), a.q, a.reverse, wave, i16, g);
             out.open(a.o, s.batch(a) * a.o_sb + s.hv * a.o_sh, row0, a.o_st, a.o_f32, a.o_vec, a.reverse, a.v.dim, 0, wave, i16, g);
             walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DV / 16];
-                out.flush();
-                row_outputs<DK, DV, false, true>(lk[b], lv[b], ls[b], d, q.f[0], wave, lane, odd, O,
+                auto late = [&] {
+                    if constexpr (WIDE) out.flush();
+                };
+                if constexpr (!WIDE) out.flush();
+                row_outputs<DK, DV, false, true>(lk[b], lv[b], ls[b], d, q.f[0], wave, lane, odd, O, late,
                                                  [&] { q.load(left - kChunk); });
                 out.put(O, left < kChunk ? left : kChunk);
             });
         } else {
             RowLoads<DV, VEC> q;
-            Output<DK> out;
+            Output<DK, WIDE> out;
             q.open(s.row(a, z.q, row0), z.q, a.reverse, wave - 4, i16, g);
             out.open(z.o, s.batch(a) * z.o_sb + s.hv * z.o_sh, row0, z.o_st, z.o_f32, z.o_vec, a.reverse, a.k.dim, 0, wave - 4, i16, g);
             walk(q, out, [&](int b, int left, bool odd) {
                 f32x4 O[DK / 16];
-                out.flush();
-                row_outputs<DV, DK, true, true>(lv[b], lk[b], ls[b], d, q.f[0], wave - 4, lane, odd, O,
+                auto late = [&] {
+                    if constexpr (WIDE) out.flush();
+                };
+                if constexpr (!WIDE) out.flush();
+                row_outputs<DV, DK, true, true>(lv[b], lk[b], ls[b], d, q.f[0], wave - 4, lane, odd, O, late,
                                                 [&] { q.load(left - kChunk); });
                 out.put(O, left < kChunk ? left : kChunk);
             });
@@ -938,20 +951,21 @@ WalkShape walk_shape(int64_t Dk, int64_t Dv) {
     return w;
 }
 
-template <int DK, int NV, int VEC>
+template <int DK, int NV, int VEC, bool WIDE>
 static hipError_t walk_go(bool states, const WalkArgs& a, hipStream_t s) {
     const uint32_t groups = static_cast<uint32_t>(a.segments * a.HV * a.vblocks);
     if (states)
         hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), dim3(groups, a.sub), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC>), dim3(groups), dim3(512), 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, WIDE>), dim3(groups), dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
 template <int DK, int NV>
 static hipError_t walk_vec(int vec, bool states, const WalkArgs& a, hipStream_t s) {
-    if (vec == 8) return walk_go<DK, NV, 8>(states, a, s);
-    return vec == 4 ? walk_go<DK, NV, 4>(states, a, s) : walk_go<DK, NV, 1>(states, a, s);
+    if (vec == 8)
+        return a.o_vec == 8 && !a.o_f32 ? walk_go<DK, NV, 8, true>(states, a, s) : walk_go<DK, NV, 8, false>(states, a, s);
+    return vec == 4 ? walk_go<DK, NV, 4, false>(states, a, s) : walk_go<DK, NV, 1, false>(states, a, s);
 }
 
 hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, hipStream_t s) {
@@ -965,12 +979,14 @@ hipError_t launch_walk(const WalkShape& w, bool states_only, const WalkArgs& a, 
 template <int DK, int DV>
 static hipError_t walk2_vec(int vec, const WalkArgs& a, const SecondWalk& z, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(a.segments * a.HV)), block(768);
-    if (vec == 8)
-        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 8>), grid, block, 0, s, a, z);
+    if (vec == 8 && a.o_vec == 8 && z.o_vec == 8 && !a.o_f32 && !z.o_f32)
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 8, true>), grid, block, 0, s, a, z);
+    else if (vec == 8)
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 8, false>), grid, block, 0, s, a, z);
     else if (vec == 4)
-        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 4>), grid, block, 0, s, a, z);
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 4, false>), grid, block, 0, s, a, z);
     else
-        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 1>), grid, block, 0, s, a, z);
+        hipLaunchKernelGGL((cconv_linattn_walk2_kernel<DK, DV, 1, false>), grid, block, 0, s, a, z);
     return hipGetLastError();
 }
 
