@@ -798,10 +798,10 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
 template <int DK, int NV, int VEC>
 __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
-    __shared__ __align__(16) uint16_t lk[kChunk * DK];
-    __shared__ __align__(16) uint16_t lv[kChunk * DVB];
+    __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
+    __shared__ __align__(16) uint16_t lv[2][kChunk * DVB];
     __shared__ Table tab;
-    __shared__ int odd_chunk;  // the chunk whose values hold an infinity or NaN
+    __shared__ int odd_chunk[2];  // the chunk whose values hold an infinity or NaN
 
     if (a.status && *a.status != CCONV_OK) return;
     Segment s;
@@ -820,21 +820,27 @@ __global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a
     Wave<DK, NV, DVB> w;
     w.open(a.log_decay[s.hv], a.gamma, a.shift);
     tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
-    if (threadIdx.x == 0) odd_chunk = -1;
+    if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
+    __syncthreads();
+    auto stage = [&](int c0) {  // a chunk to LDS, the one after it to registers
+        const int b = (c0 / kChunk) & 1;
+        sk.store(lk[b]);
+        sv.store(lv[b]);
+        if (sv.special()) odd_chunk[b] = c0;
+        if (c0 + kChunk >= rows) return;
+        sk.load(kChunk);
+        sv.load(kChunk);
+    };
+    stage(0);
+    lds_barrier();
     float more = 1.0f;
     for (int c0 = 0; c0 < rows; c0 += kChunk) {
-        lds_barrier();
-        sk.store(lk);
-        sv.store(lv);
-        if (sv.special()) odd_chunk = c0;
-        lds_barrier();
-        if (rows - c0 > kChunk) {
-            sk.load(kChunk);
-            sv.load(kChunk);
-        }
-        const bool sv_special = __builtin_amdgcn_readfirstlane(odd_chunk) == c0;
-        w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lv, wave * NV, tab, kChunk, sv_special, more);
+        const int b = (c0 / kChunk) & 1;
+        const bool special = __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0;
+        if (c0 + kChunk < rows) stage(c0 + kChunk);
+        w.template update<false, DK == 256 ? 4 : DK / 16>(lk[b], lv[b], wave * NV, tab, kChunk, special, more);
         more *= w.aC;
+        lds_barrier();
     }
     float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
                (wave * 64 + lane) * 4;
