@@ -396,6 +396,7 @@ cconv_status_t cconv_linattn_bwd(const cconv_rows_t* q, const cconv_rows_t* k, c
         g.o_sb = r.sb, g.o_st = r.st, g.o_sh = r.sh;
         g.B = B, g.T = T;
         g.H = static_cast<int>(H), g.grp = grp, g.dim = static_cast<int>(Dk);
+        g.vec = row_vec(r, nk) >= 4 ? 4 : 1;
         g.status = base.status;
         return launch_group_sum(g, s) == hipSuccess ? CCONV_OK : CCONV_ERR_LAUNCH;
     };

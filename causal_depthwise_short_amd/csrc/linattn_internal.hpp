@@ -94,7 +94,7 @@ struct GroupSumArgs {
     uint16_t* out;
     int64_t o_sb, o_st, o_sh;
     int64_t B, T;
-    int H, grp, dim;
+    int H, grp, dim, vec;
     const int32_t* status;
 };
 hipError_t launch_group_sum(const GroupSumArgs& a, hipStream_t s);

@@ -519,8 +519,11 @@ struct Segment {
     int64_t seq, seg, start, len, first, rows;
     int hv, vb;
     bool last;
-    __device__ __forceinline__ bool open(const WalkArgs& a) {
-        const uint32_t tile = static_cast<uint32_t>(xcd_tile(blockIdx.x, gridDim.x));
+    // `sums`: the grid has no place for the last segment of each sequence (fixed lengths).
+    // Neighbouring tiles, which share q and k or their lines, go to one XCD, except in packed batches, whose
+    // last places may be empty: an XCD would have nothing but those.
+    __device__ __forceinline__ bool open(const WalkArgs& a, bool sums = false) {
+        const uint32_t tile = a.cu ? blockIdx.x : static_cast<uint32_t>(xcd_tile(blockIdx.x, gridDim.x));
         const uint32_t per_seg = static_cast<uint32_t>(a.vblocks * a.HV), hvb = tile % per_seg;
         vb = static_cast<int>(hvb % a.vblocks), hv = static_cast<int>(hvb / a.vblocks);
         seg = tile / per_seg;
@@ -531,8 +534,11 @@ struct Segment {
             start = a.cu[seq];
             len = a.cu[seq + 1] - start;
         } else {
-            seq = static_cast<uint32_t>(seg) / static_cast<uint32_t>(a.segs);
-            first = (seg - seq * a.segs) * a.seg_rows;
+            const uint32_t each = static_cast<uint32_t>(a.segs) - (sums ? 1 : 0);
+            seq = static_cast<uint32_t>(seg) / each;
+            const int64_t k = seg - seq * each;
+            seg = seq * a.segs + k;
+            first = k * a.seg_rows;
             start = 0;
             len = a.T;
         }
@@ -794,53 +800,87 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
 // Each segment's own sum of k^T v, for the segments that another follows. The chunks are taken from the
 // segment's last to its first: their weights then only grow smaller, so the state needs no scaling, and
 // the rows read last are those that the walk after it reads first. A segment is summed in `sub` parts, each
-// by a workgroup of its own.
+// by a workgroup of its own, in which GROUPS sets of four waves take every GROUPS-th chunk: a set alone on its
+// CU has nothing to do while it waits for its own loads.
 template <int DK, int NV, int VEC>
-__global__ __launch_bounds__(256, 2) void cconv_linattn_states_kernel(WalkArgs a) {
-    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16;
-    __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
-    __shared__ __align__(16) uint16_t lv[2][kChunk * DVB];
+__global__ __launch_bounds__(DK == 256 ? 256 : 512, DK == 256 ? 1 : 2) void cconv_linattn_states_kernel(WalkArgs a) {
+    constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16, GROUPS = DK == 256 ? 1 : 2;
+    constexpr int kTile = kChunk * (DK + DVB);  // a chunk's k and v
+    // the sets' chunks, two each; after the last chunk, the sums on their way to the first set
+    __shared__ __align__(16) uint16_t lds[GROUPS * 2 * kTile];
+    static_assert(sizeof(lds) >= DK * DVB * sizeof(float), "");
     __shared__ Table tab;
-    __shared__ int odd_chunk[2];  // the chunk whose values hold an infinity or NaN
+    __shared__ int odd_chunk[GROUPS][2];  // the chunk whose values hold an infinity or NaN
 
     if (a.status && *a.status != CCONV_OK) return;
     Segment s;
     const int part = static_cast<int>(blockIdx.y);
-    if (!s.open(a) || s.last) return;  // (so the segment is whole)
-    const int rows = static_cast<int>(s.rows) / a.sub, end = rows * (part + 1) - kChunk;
+    if (!s.open(a, true) || s.last) return;  // (so the segment is whole)
+    const int wave = wave_id() % 4, group = wave_id() / 4, lane = threadIdx.x % kWave;
+    const int rows = static_cast<int>(s.rows) / a.sub, chunks = rows / kChunk;
+    const int end = rows * (part + 1) - (1 + group) * kChunk;  // the set's first chunk
     const int64_t row0 = s.row0(a.reverse) + (a.reverse ? -end : end);
     Stage<DK, VEC, 256> sk;
     Stage<DVB, VEC, 256> sv;
     sk.open(s.row(a, a.k, row0), a.k, a.reverse, 0);
     sv.open(s.row(a, a.v, row0), a.v, a.reverse, s.vb * DVB);
-    sk.step = -sk.step, sv.step = -sv.step;
-    sk.load(kChunk);
-    sv.load(kChunk);
-    const int wave = wave_id(), lane = threadIdx.x % kWave;
+    sk.step *= -GROUPS, sv.step *= -GROUPS;
+    if (group < chunks) {
+        sk.load(kChunk);
+        sv.load(kChunk);
+    }
     Wave<DK, NV, DVB> w;
     w.open(a.log_decay[s.hv], a.gamma, a.shift);
     tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
-    if (threadIdx.x < 2) odd_chunk[threadIdx.x] = -1;
+    if (threadIdx.x < 2 * GROUPS) (&odd_chunk[0][0])[threadIdx.x] = -1;
     __syncthreads();
-    auto stage = [&](int c0) {  // a chunk to LDS, the one after it to registers
-        const int b = (c0 / kChunk) & 1;
-        sk.store(lk[b]);
-        sv.store(lv[b]);
-        if (sv.special()) odd_chunk[b] = c0;
-        if (c0 + kChunk >= rows) return;
+    uint16_t* mine = lds + group * 2 * kTile;
+    auto stage = [&](int c, int b) {  // chunk c to LDS, the set's one after it to registers
+        uint16_t* lk = mine + b * kTile;
+        sk.store(lk);
+        sv.store(lk + kChunk * DK);
+        if (sv.special()) odd_chunk[group][b] = c;
+        if (c + GROUPS >= chunks) return;
         sk.load(kChunk);
         sv.load(kChunk);
     };
-    stage(0);
+    if (group < chunks) stage(group, 0);
     lds_barrier();
-    float more = 1.0f;
-    for (int c0 = 0; c0 < rows; c0 += kChunk) {
-        const int b = (c0 / kChunk) & 1;
-        const bool special = __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0;
-        if (c0 + kChunk < rows) stage(c0 + kChunk);
-        w.template update<false, DK == 256 ? 4 : DK / 16>(lk[b], lv[b], wave * NV, tab, kChunk, special, more);
-        more *= w.aC;
+    float more = 1.0f, skip = w.aC;
+    if (GROUPS == 2) {
+        if (group == 1) more = w.aC;
+        skip = w.aC * w.aC;
+    }
+    int b = 0;
+    for (int c0 = 0; c0 < chunks; c0 += GROUPS, b ^= 1) {
+        const int c = c0 + group;
+        const bool special = __builtin_amdgcn_readfirstlane(odd_chunk[group][b]) == c;
+        if (c + GROUPS < chunks) stage(c + GROUPS, b ^ 1);
+        if (c < chunks) {
+            const uint16_t* lk = mine + b * kTile;
+            w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lk + kChunk * DK, wave * NV, tab, kChunk, special, more);
+        }
+        more *= skip;
         lds_barrier();
+    }
+    if (GROUPS == 2) {
+        f32x4* x = reinterpret_cast<f32x4*>(lds) + wave * 64 + lane;
+        if (group == 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int m = 0; m < NM; ++m) x[(t * NM + m) * 256] = w.S[t][m];
+        }
+        lds_barrier();
+        if (group == 1) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const f32x4 y = x[(t * NM + m) * 256];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w.S[t][m][r] += y[r];
+            }
     }
     float* c = a.states + ((s.seg * a.sub + part) * a.HV + s.hv) * static_cast<int64_t>(a.vblocks) * DK * DVB + s.vb * DK * DVB +
                (wave * 64 + lane) * 4;
@@ -937,15 +977,32 @@ __global__ __launch_bounds__(1024) void cconv_linattn_plan_kernel(const int32_t*
     for (int64_t s = used + threadIdx.x; s < segments; s += blockDim.x) seg_of[2 * s] = -1;
 }
 
+// VEC channels a thread (4: rows of whole groups of four channels, 4-byte aligned).
+template <int VEC>
 __global__ __launch_bounds__(256) void cconv_linattn_group_sum_kernel(GroupSumArgs a) {
     if (a.status && *a.status != CCONV_OK) return;
-    const int64_t total = a.B * a.T * a.H * a.dim;
+    const uint32_t per = static_cast<uint32_t>(a.dim / VEC), per_row = per * static_cast<uint32_t>(a.H);
+    const int64_t total = a.B * a.T * per_row;
     for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total; e += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t c = e % a.dim, h = e / a.dim % a.H, row = e / (static_cast<int64_t>(a.dim) * a.H);
+        const int64_t row = e / per_row, b = row / a.T;
+        const uint32_t in = static_cast<uint32_t>(e - row * per_row), h = in / per, c = (in - h * per) * VEC;
         const float* p = a.part + (row * a.H + h) * a.grp * a.dim + c;
-        float s = p[0];
-        for (int g = 1; g < a.grp; ++g) s += p[static_cast<int64_t>(g) * a.dim];
-        a.out[row / a.T * a.o_sb + row % a.T * a.o_st + h * a.o_sh + c] = static_cast<uint16_t>(pack_bf16x2(s, 0.0f) & 0xffffu);
+        uint16_t* o = a.out + b * a.o_sb + (row - b * a.T) * a.o_st + h * a.o_sh + c;
+        if constexpr (VEC == 4) {
+            f32x4 s = *reinterpret_cast<const f32x4*>(p);
+            for (int g = 1; g < a.grp; ++g) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(g) * a.dim);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] += x[r];
+            }
+            u32x2a w;
+            w.x = pack_bf16x2(s[0], s[1]), w.y = pack_bf16x2(s[2], s[3]);
+            *reinterpret_cast<u32x2a*>(o) = w;
+        } else {
+            float s = p[0];
+            for (int g = 1; g < a.grp; ++g) s += p[static_cast<int64_t>(g) * a.dim];
+            *o = static_cast<uint16_t>(pack_bf16x2(s, 0.0f) & 0xffffu);
+        }
     }
 }
 
@@ -960,8 +1017,9 @@ WalkShape walk_shape(int64_t Dk, int64_t Dv) {
 template <int DK, int NV, int VEC, bool WIDE>
 static hipError_t walk_go(bool states, const WalkArgs& a, hipStream_t s) {
     const uint32_t groups = static_cast<uint32_t>(a.segments * a.HV * a.vblocks);
+    const uint32_t sums = a.cu ? groups : static_cast<uint32_t>(a.segments / a.segs * (a.segs - 1) * a.HV * a.vblocks);
     if (states)
-        hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), dim3(groups, a.sub), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((cconv_linattn_states_kernel<DK, NV, VEC>), dim3(sums, a.sub), dim3(DK == 256 ? 256 : 512), 0, s, a);
     else
         hipLaunchKernelGGL((cconv_linattn_walk_kernel<DK, NV, VEC, WIDE>), dim3(groups), dim3(512), 0, s, a);
     return hipGetLastError();
@@ -1018,9 +1076,12 @@ hipError_t launch_seg_plan(const int32_t* cu, int64_t nseq, int64_t total, int64
 }
 
 hipError_t launch_group_sum(const GroupSumArgs& a, hipStream_t s) {
-    const int64_t blocks = (a.B * a.T * a.H * a.dim + 255) / 256;
-    hipLaunchKernelGGL(cconv_linattn_group_sum_kernel, dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), dim3(256),
-                       0, s, a);
+    const int64_t blocks = (a.B * a.T * a.H * a.dim / a.vec + 255) / 256;
+    const dim3 grid(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)), block(256);
+    if (a.vec == 4)
+        hipLaunchKernelGGL(cconv_linattn_group_sum_kernel<4>, grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL(cconv_linattn_group_sum_kernel<1>, grid, block, 0, s, a);
     return hipGetLastError();
 }
 

@@ -1,0 +1,166 @@
+"""A linear-attention layer on the library's operators, as a model runs it: trained, prefilled with packed
+prompts, and decoded token by token.
+
+    rows = x W_in                                     one fused projection, rows q | k | v
+    rows = silu(short convolution(rows))              cconv_fwd_ex / cconv_update
+    q, k = norm and rotation of every head            cconv_qknorm_fwd
+    o    = linear attention with a decay per head     cconv_linattn_fwd / _update
+    y    = o W_out
+
+q, k and v are slices of the fused rows: nothing is copied between the operators. Run it on an MI355X:
+
+    python examples/linear_attention_layer.py
+
+It trains the layer for a few steps on a fixed batch (the loss has to fall), then checks that prompts
+prefilled as one packed batch and continued token by token give the rows of a full forward.
+"""
+
+from __future__ import annotations
+
+import sys
+from pathlib import Path
+
+import torch
+
+sys.path.insert(0, str(Path(__file__).resolve().parent.parent))
+
+import causal_depthwise_short_amd as cc  # noqa: E402
+
+BF = torch.bfloat16
+
+
+class Layer:
+    """Weights of one layer: H query/key heads of Dk channels, HV value heads of Dv channels."""
+
+    def __init__(self, width: int, H: int, HV: int, Dk: int, Dv: int, positions: int, *, W: int = 4, seed: int = 0, device="cuda"):
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+        self.H, self.HV, self.Dk, self.Dv, self.W = H, HV, Dk, Dv, W
+        self.D = 2 * H * Dk + HV * Dv
+        n = lambda *s, size: torch.randn(*s, generator=g, device=device) * size  # noqa: E731
+        # trained in fp32, used in bf16
+        self.w = {"w_in": n(width, self.D, size=width**-0.5), "taps": n(self.D, W, size=0.5), "wq": torch.ones(Dk, device=device),
+                  "wk": torch.ones(Dk, device=device), "w_out": n(HV * Dv, width, size=(HV * Dv)**-0.5)}
+        self.log_decay = -torch.exp2(-8.0 * (torch.arange(HV, device=device) + 1) / HV)
+        angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * 10000.0 ** (
+            -torch.arange(0, Dk, 2, dtype=torch.float64, device=device) / Dk)
+        self.table = torch.cat([angle.cos(), angle.sin()], -1).float()
+        self.scale = Dk**-0.5
+
+    def low(self, name):
+        return self.w[name].to(BF)
+
+    def cut(self, rows):
+        """q, k, v as heads of the fused rows [..., D] (views)."""
+        a, b = self.H * self.Dk, 2 * self.H * self.Dk
+        return (rows[..., :a].unflatten(-1, (self.H, self.Dk)), rows[..., a:b].unflatten(-1, (self.H, self.Dk)),
+                rows[..., b:].unflatten(-1, (self.HV, self.Dv)))
+
+    # ---- training ----
+
+    def forward(self, x):
+        """x [B, T, width] -> (y [B, T, width], what the backward needs)."""
+        taps = self.low("taps")
+        z = x.to(BF) @ self.low("w_in")
+        rows = cc.cconv_fwd(z, taps)
+        q, k, v = self.cut(rows)
+        qn, kn, _ = cc.cconv_qknorm_fwd(q, k, self.w["wq"], self.w["wk"], self.table)
+        o, _, _ = cc.cconv_linattn_fwd(qn, kn, v, self.log_decay, scale=self.scale)
+        return o.flatten(2) @ self.low("w_out"), (x, z, taps, rows, qn, kn, o)
+
+    def backward(self, saved, dy):
+        """Gradients of every weight for dy [B, T, width]."""
+        x, z, taps, rows, qn, kn, o = saved
+        q, k, v = self.cut(rows)
+        flat = lambda t: t.flatten(0, 1)  # noqa: E731
+        d_out = flat(o.flatten(2)).T.contiguous() @ flat(dy)
+        do = (dy @ self.low("w_out").T.contiguous()).unflatten(-1, (self.HV, self.Dv))
+        dqn, dkn, dv, _, _ = cc.cconv_linattn_bwd(qn, kn, v, self.log_decay, do, scale=self.scale)
+        dq, dk, dwq, dwk, _ = cc.cconv_qknorm_bwd(q, k, dqn, dkn, self.w["wq"], self.w["wk"], self.table)
+        drows = torch.cat([dq.flatten(2), dk.flatten(2), dv.flatten(2)], -1)
+        dz, dtaps, _ = cc.cconv_bwd(z, drows, taps, want_dbias=False, dw_dtype=torch.float32)
+        d_in = flat(x.to(BF)).T.contiguous() @ flat(dz)
+        return {"w_in": d_in.float(), "taps": dtaps, "wq": dwq, "wk": dwk, "w_out": d_out.float()}
+
+    # ---- serving ----
+
+    def new_pool(self, slots: int):
+        """Decode states of `slots` sequences: (convolution, attention)."""
+        dev = self.table.device
+        return (torch.zeros(slots, self.D, self.W - 1, dtype=BF, device=dev),
+                torch.zeros(slots, self.HV, self.Dk, self.Dv, device=dev))
+
+    def prefill(self, x, cu_seqlens, positions, pool, slots):
+        """Packed prompts x [total, width] into the pool's slots; y [total, width]."""
+        z = x.to(BF) @ self.low("w_in")
+        rows, conv, s0 = cc.cconv_fwd_ex(z, self.low("taps"), cu_seqlens=cu_seqlens, want_final_state=True)
+        q, k, v = self.cut(rows)
+        qn, kn, s1 = cc.cconv_qknorm_fwd(q[None], k[None], self.w["wq"], self.w["wk"], self.table, positions=positions[None])
+        o, state, s2 = cc.cconv_linattn_fwd(qn[0], kn[0], v, self.log_decay, scale=self.scale, want_final_state=True,
+                                            cu_seqlens=cu_seqlens)
+        pool[0][slots.long()], pool[1][slots.long()] = conv, state
+        return o.flatten(1) @ self.low("w_out"), (s0, s1, s2)
+
+    def decode(self, x, positions, pool, slots):
+        """One token of every sequence, x [N, width]; the pool's states advance in place."""
+        z = x.to(BF) @ self.low("w_in")
+        rows, s0 = cc.cconv_update(z, pool[0], slots, self.low("taps"))
+        q, k, v = self.cut(rows)
+        qn, kn, s1 = cc.cconv_qknorm_fwd(q[:, None], k[:, None], self.w["wq"], self.w["wk"], self.table, positions=positions[:, None])
+        o, s2 = cc.cconv_linattn_update(qn[:, 0], kn[:, 0], v, self.log_decay, pool[1], slots, scale=self.scale)
+        return o.flatten(1) @ self.low("w_out"), (s0, s1, s2)
+
+
+def train(layer: Layer, x, target, steps: int = 20, rate: float = 0.02):
+    """Sign-descent steps on a fixed batch; the losses."""
+    losses = []
+    for _ in range(steps):
+        y, saved = layer.forward(x)
+        d = y.float() - target
+        losses.append(float(d.square().mean()))
+        grads = layer.backward(saved, (2 * d / d.numel()).to(BF))
+        for name, g in grads.items():
+            layer.w[name] -= rate * layer.w[name].square().mean().sqrt() * g.sign()
+    return losses
+
+
+def serve(layer: Layer, lengths, tokens: int, seed: int = 1):
+    """Prefills prompts of these lengths as one packed batch, decodes `tokens` more of each, and returns
+    (the rows so made, the rows of a full forward) of every sequence."""
+    dev = layer.table.device
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    width = layer.w["w_in"].shape[0]
+    xs = [torch.randn(n + tokens, width, generator=g, device=dev).to(BF) for n in lengths]
+    n = len(lengths)
+    pool, slots = layer.new_pool(2 * n), torch.arange(2 * n - 1, n - 1, -1, dtype=torch.int32, device=dev)
+    cu = torch.tensor([0, *torch.tensor(lengths).cumsum(0).tolist()], dtype=torch.int32, device=dev)
+    at = torch.cat([torch.arange(m, dtype=torch.int32) for m in lengths]).to(dev)
+    y, status = layer.prefill(torch.cat([x[:m] for x, m in zip(xs, lengths)]), cu, at, pool, slots)
+    made = [[y[cu[i]:cu[i + 1]]] for i in range(n)]
+    for t in range(tokens):
+        pos = torch.tensor([m + t for m in lengths], dtype=torch.int32, device=dev)
+        y, status = layer.decode(torch.stack([x[m + t] for x, m in zip(xs, lengths)]), pos, pool, slots)
+        for i in range(n):
+            made[i].append(y[i:i + 1])
+    assert all(int(s) == 0 for s in status if s is not None)
+    return [torch.cat(m) for m in made], [layer.forward(x[None])[0][0] for x in xs]
+
+
+def main():
+    layer = Layer(width=512, H=4, HV=8, Dk=128, Dv=128, positions=4096)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.randn(2, 700, 512, generator=g, device="cuda")
+    losses = train(layer, x, torch.roll(x, 3, 1))
+    print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps")
+    assert losses[-1] < 0.9 * losses[0]
+    made, full = serve(layer, [5, 300, 64, 1], tokens=12)
+    # each side rounds every stage to bf16, and the two round their products' operands at other places
+    worst = max(float((m.float() - f.float()).norm() / f.float().norm()) for m, f in zip(made, full))
+    print(f"prefill and decode against the full forward: relative difference {worst:.1e}")
+    assert worst < 0.02
+
+
+if __name__ == "__main__":
+    main()
