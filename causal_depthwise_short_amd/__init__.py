@@ -1,4 +1,6 @@
-"""Python binding of libcconv.so: the depthwise causal short convolution + SiLU on MI355X.
+"""Python binding of libcconv.so: the depthwise causal short convolution + SiLU on MI355X, and the
+layer's operators around it (linear attention with a decay for each head, the norm of query and key heads
+with the position rotation).
 
 Argument marshalling only. Every function here checks that its torch tensors are device
 tensors of the dtype and layout the C ABI expects, allocates outputs with ``torch.empty``

@@ -5,7 +5,9 @@
 // by that traffic. A thread owns VEC neighbouring value channels of every (256 / CL)-th key, so a
 // wave's loads and stores cover whole rows, and the first kRows rows' loads are in flight before
 // the slot check and the operands' loads are waited for. The partial sums of o over the keys meet in
-// LDS and are added in a fixed order.
+// LDS and are added in a fixed order. The state's loads and stores are non-temporal (a pool of a serving batch
+// is larger than the caches: 155 -> 146 us). 146 us for the 760 MB of 180 live rows of 32 heads of
+// 128 x 128, 5.2 TB/s; one row of 16 heads takes 5 us.
 #include "../../include/cconv.h"
 #include "cconv_device.hpp"
 #include "linattn_internal.hpp"
@@ -140,7 +142,8 @@ static hipError_t step_go(const StepArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_step(const StepArgs& a, bool vec4, hipStream_t s) {
-    // few rows: narrower column blocks, so that more of the chip takes part
+    // few rows: narrower column blocks, so that more of the chip takes part (one row of 16 heads 5.1 us against
+    // 5.9 us; 192 rows of 32 heads 153 us against 145 us)
     const bool few = a.N * a.HV < 256;
     if (vec4) return few ? step_go<4, 8>(a, s) : step_go<4, 32>(a, s);
     return few ? step_go<1, 16>(a, s) : step_go<1, 64>(a, s);

@@ -15,8 +15,9 @@
 //   * four row waves make the outputs, 16 rows each: scores against the chunk's earlier rows, products
 //     with the state's copy, products with v.
 // k, v and the copy of the state are double-buffered, so a chunk costs one barrier, and its time is the
-// longer of the two waves' parts, not their sum (with every wave doing both parts in turn, three barriers
-// a chunk, a chunk took 4.5 us; see the figures at the kernels).
+// longer of the two waves' parts, not their sum. At 128 channels a side a workgroup alone on its CU takes
+// 2.9 us a chunk (5300 cycles of row waves, 5500 of state waves); with every wave doing both parts in turn and
+// three barriers a chunk it took 4.5 us, and the walk of [4, 8192, 32 heads, 128] 244 us instead of 204 us.
 // Every product is laid out so that what one leaves in registers is what the next takes: scores as
 // p^T[m = row j][n = row i] are the right operand of o^T = v^T p^T, with v read from LDS by the transposing
 // loads; rows of q go from memory straight to fragments.
@@ -215,9 +216,6 @@ struct Wave {
 #pragma unroll
             for (int m = 0; m < NM; ++m) S[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    // row of element e of a transposed fragment, within its 32 rows
-    __device__ __forceinline__ int row_of(int e) const { return 4 * g + (e & 3) + 16 * (e >> 2); }
-
     // The bf16 copy for the row waves: a row of DK keys for each value channel, from row row0 on.
     __device__ __forceinline__ void publish(uint16_t* ls, int row0) const {
         const int lane = anew(threadIdx.x % kWave, LEAN), i16 = lane % 16, g = lane / 16;
@@ -606,7 +604,9 @@ __device__ __forceinline__ void enter(Wave<DK, NV, COLSV, LEAN>& w, const WalkAr
 }
 
 // The walk: four row waves, then four state waves, of NV value channels each, which also stage the chunks
-// (the row waves' part is the longer).
+// (staged by all eight, the row waves' part was the longer: 242 us instead of 216 us). 204 us at
+// [4, 8192, 32 heads, 128] for the 1.08 GB of q, k, v and o, 5.3 TB/s: near what memory gives, with the
+// matrix units at 32% and the vector units at 54%.
 template <int DK, int NV, int VEC, bool WIDE>
 __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV;
@@ -696,7 +696,9 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 
 // Two walks over the same rows whose states are each other's transposes: dv (rows k, keys q, values do)
 // and dk (rows v, keys do, values q). One set of state waves serves both, the second set of row waves
-// reading the state's copy by columns; q and do are staged once.
+// reading the state's copy by columns; q and do are staged once. 340 us at [4, 8192, 32 heads, 128] for the
+// 1.61 GB of q, k, v, do, dk and dv, 4.7 TB/s; as two walks they took 2 x 244 us and a second pass for the
+// segments' sums. Three waves on every SIMD leave each 168 registers: a few row addresses spill.
 template <int DK, int DV, int VEC, bool WIDE>
 __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a, SecondWalk z) {
     constexpr int NV = DV / 4;
@@ -801,7 +803,8 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
 // segment's last to its first: their weights then only grow smaller, so the state needs no scaling, and
 // the rows read last are those that the walk after it reads first. A segment is summed in `sub` parts, each
 // by a workgroup of its own, in which GROUPS sets of four waves take every GROUPS-th chunk: a set alone on its
-// CU has nothing to do while it waits for its own loads.
+// CU has nothing to do while it waits for its own loads. 68 us for the 268 MB of k and v of the first halves of
+// [4, 8192, 32 heads, 128], 3.9 TB/s, bound by the latency of a set's chunk.
 template <int DK, int NV, int VEC>
 __global__ __launch_bounds__(DK == 256 ? 256 : 512, DK == 256 ? 1 : 2) void cconv_linattn_states_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV, NM = NV / 16, NT = DK / 16, GROUPS = DK == 256 ? 1 : 2;
@@ -1009,7 +1012,8 @@ __global__ __launch_bounds__(256) void cconv_linattn_group_sum_kernel(GroupSumAr
 WalkShape walk_shape(int64_t Dk, int64_t Dv) {
     WalkShape w;
     w.DK = Dk <= 64 ? 64 : Dk <= 128 ? 128 : 256;
-    // 256 keys: 16 value channels a wave keep the state at 64 registers
+    // Blocks of 128 value channels rather than two of 64, which both read q and k: 258 us against 290 us for a
+    // walk at [4, 8192, 32 heads, 128]. With 256 keys 16 channels a wave keep the state at 64 registers.
     w.NV = (w.DK <= 128 && Dv > 64) ? 32 : 16;
     return w;
 }
