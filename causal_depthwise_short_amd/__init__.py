@@ -1086,6 +1086,16 @@ def _decay(log_decay, HV: int) -> int:
     return _plain(log_decay, "log_decay", "fp32 [HV]", torch.float32, (HV,))
 
 
+def _used_on(stream, *tensors):
+    """Tells torch's allocator that these tensors, made on the current stream, are used on the caller's: without
+    that a workspace freed on return could be handed out again while the call still runs."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _workspace(t, need: int, like):
     """The caller's workspace, or a new one next to `like`; (tensor or None, address, bytes)."""
     if t is None:
@@ -1157,6 +1167,8 @@ def cconv_linattn_fwd(q, k, v, log_decay, *, scale: float = 1.0, init_state=None
     workspace, ws, ws_bytes = _workspace(workspace, L.cconv_linattn_fwd_workspace_bytes(B, T, nseq, HV, Dk, Dv), q)
     _check(L.cconv_linattn_fwd(rq, rk, rv, ld, scale, _ptr(init_state), ro, _ptr(final_state), _ptr(cu_seqlens), nseq,
                                _ptr(status), ws, ws_bytes, B, T, H, HV, Dk, Dv, _stream(stream)), "cconv_linattn_fwd")
+    if stream is not None:
+        _used_on(stream, o, final_state, status, workspace)
     return o, final_state, status
 
 
@@ -1196,6 +1208,8 @@ def cconv_linattn_bwd(q, k, v, log_decay, d_o, *, scale: float = 1.0, init_state
     _check(L.cconv_linattn_bwd(rq, rk, rv, ld, scale, _ptr(init_state), rdo, _ptr(d_final_state), *outs,
                                _ptr(d_init_state), _ptr(cu_seqlens), nseq, _ptr(status), ws, ws_bytes, B, T,
                                H, HV, Dk, Dv, _stream(stream)), "cconv_linattn_bwd")
+    if stream is not None:
+        _used_on(stream, dq, dk, dv, d_init_state, status, workspace)
     return dq, dk, dv, d_init_state, status
 
 
@@ -1225,6 +1239,8 @@ def cconv_linattn_update(q, k, v, log_decay, state, state_indices=None, *, scale
         _out(status, "status", (1,), _I32)
     _check(lib().cconv_linattn_update(rq, rk, rv, ld, scale, pool, state.shape[0], idx, ro, N, H, HV, Dk, Dv,
                                       status.data_ptr(), _stream(stream)), "cconv_linattn_update")
+    if stream is not None:
+        _used_on(stream, o, status)
     return o, status
 
 
@@ -1283,6 +1299,8 @@ def cconv_qknorm_fwd(q, k, wq, wk, table=None, *, positions=None, eps: float = 1
         ps = status.data_ptr()
     _check(lib().cconv_qknorm_fwd(rq, rk, pq, pk, wdt, pt, P, R, interleaved, pp, eps, ryq, ryk, B, T, Hq, k.shape[2], D, ps,
                                   _stream(stream)), "cconv_qknorm_fwd")
+    if stream is not None:
+        _used_on(stream, yq, yk, status)
     return yq, yk, status
 
 
@@ -1321,4 +1339,6 @@ def cconv_qknorm_bwd(q, k, dyq, dyk, wq, wk, table=None, *, positions=None, eps:
     workspace, ws, ws_bytes = _workspace(workspace, L.cconv_qknorm_bwd_workspace_bytes(B, T, Hq, Hk, D), q)
     _check(L.cconv_qknorm_bwd(rq, rk, rdyq, rdyk, pq, pk, wdt, pt, P, R, interleaved, pp, eps, rdq, rdk, pdwq, pdwk, ws, ws_bytes,
                               B, T, Hq, Hk, D, ps, _stream(stream)), "cconv_qknorm_bwd")
+    if stream is not None:
+        _used_on(stream, dq, dk, dwq, dwk, status, workspace)
     return dq, dk, dwq, dwk, status

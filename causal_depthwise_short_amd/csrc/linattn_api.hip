@@ -17,7 +17,7 @@ using namespace cconv;
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 40;    // any size times a stride stays far below 2^63
-constexpr int64_t kMaxRowCount = int64_t(1) << 31;  // rows of a packed batch (32-bit offsets)
+constexpr int64_t kMaxRowCount = int64_t(1) << 30;  // rows of one sequence or packed batch (32-bit row counters)
 constexpr int64_t kMaxWalkStride = int64_t(1) << 22;  // a chunk's 64 rows (fp32 at most) stay within 31 bits of bytes
 constexpr int64_t kMaxHeads = int64_t(1) << 14;
 constexpr int64_t kMaxHeadDim = 256;
@@ -526,7 +526,7 @@ size_t norm_ws(int64_t B, int64_t T, int64_t D) {
 
 cconv_status_t norm_impl(NormCall c, hipStream_t s) {
     if (c.B < 0 || c.T < 0 || c.Hq < 1 || c.Hk < 1 || c.D < 1 || c.D > kMaxHeadDim || c.Hq > kMaxHeads || c.Hk > kMaxHeads ||
-        c.P < 0 || c.P > kMaxRowCount || c.R < 0 || c.R % 2 != 0 || c.R > c.D || c.B > kMaxSequences || c.T >= kMaxRowCount)
+        c.P < 0 || c.P > (int64_t(1) << 31) || c.R < 0 || c.R % 2 != 0 || c.R > c.D || c.B > kMaxSequences || c.T >= kMaxRowCount)
         return CCONV_ERR_BAD_SHAPE;
     const __int128 rows = static_cast<__int128>(c.B) * c.T;
     if (rows > (static_cast<__int128>(1) << 32)) return CCONV_ERR_BAD_SHAPE;

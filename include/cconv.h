@@ -513,7 +513,7 @@ cconv_status_t cconv_bwd_varlen_config(const void* x, int64_t x_st, const void* 
  * head, and the norm of query and key heads with the position rotation. The conventions at the
  * top of this file hold (caller-owned memory, work only enqueued on `stream`, capturable, fp32
  * states, errors before anything is enqueued, a device status word for what only the device sees).
- * Dimensions: 1 <= Dk, Dv, D <= 256; 1 <= H, HV, Hq, Hk <= 2^14; empty batches (B, T or N zero) are CCONV_OK.
+ * Dimensions: 1 <= Dk, Dv, D <= 256; 1 <= H, HV, Hq, Hk <= 2^14; T < 2^30; empty batches (B, T or N zero) are CCONV_OK.
  *
  * cconv_rows_t: bf16 rows of heads, element (b, t, h, c) at p + b*sb + t*st + h*sh + c (elements,
  * channels contiguous, strides >= 0, so a slice of a fused projection, a [B, H, T, D] layout or a

@@ -347,6 +347,49 @@ def test_prompt_then_tokens_equals_the_longer_prompt():
     close_state(fin, layer.linattn(*args)[1], layer.linattn_size(*args)[1], "state")
 
 
+# ---- offsets past 32 bits ------------------------------------------------------------------
+
+
+def test_rows_past_32_bit_offsets():
+    """2.2e9 elements a tensor: the last rows of a long sequence with fast decays equal those of its tail alone
+    (rows 1024 back weigh e^-512), forwards and backwards."""
+    T, H, tail, keep = 270000, 64, 1600, 400
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.empty(1, T, H, 128, dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 2**31
+    for i in range(0, T, 30000):
+        x[:, i:i + 30000] = torch.randn(1, 30000, H, 128, generator=g, device=DEV).to(torch.bfloat16)
+    ld = torch.full((H,), -0.5, device=DEV)
+    o, fin, _ = cc.cconv_linattn_fwd(x, x, x, ld, want_final_state=True)
+    y = x[:, -tail:]
+    p, f2, _ = cc.cconv_linattn_fwd(y, y, y, ld, want_final_state=True)
+    # each side rounds its scores, its state and its result: 2 * 0.82 u of the norm at most
+    a, b = o[:, -keep:].float(), p[:, -keep:].float()
+    assert float((a - b).norm()) <= 2 * U * float(b.norm())
+    assert float((fin - f2).norm()) <= 2.0**-16 * float(f2.norm())
+    del o
+    got = cc.cconv_linattn_bwd(x, x, x, ld, x, want_d_init_state=False)[:3]
+    want = cc.cconv_linattn_bwd(y, y, y, ld, y)[:3]
+    for a, b in zip(got, want):
+        a, b = a[:, -keep:].float(), b[:, -keep:].float()
+        assert float((a - b).norm()) <= 2 * U * float(b.norm())
+
+
+def test_pool_past_32_bit_offsets():
+    pool = torch.zeros(2200, 32, 128, 128, device=DEV)
+    assert pool.numel() * 4 > 2**32
+    q, k, v, ld, _ = make((2, 32, 128), (2, 32, 128), 3)
+    idx = torch.tensor([2199, 7], dtype=torch.int32, device=DEV)
+    o, st = cc.cconv_linattn_update(q.to(DEV), k.to(DEV), v.to(DEV), ld.to(DEV), pool, idx)
+    assert int(st) == 0
+    want = f64(k)[..., :, None] * f64(v)[..., None, :]
+    for n, i in enumerate((2199, 7)):  # a product of two bf16 values is exact in fp32
+        assert np.array_equal(f64(pool[i]), want[n])
+        pool[i] = 0
+    assert not pool.any()
+
+
 # ---- streams and graphs --------------------------------------------------------------------
 
 
@@ -390,6 +433,27 @@ def test_another_stream():
     got, _, _ = cc.cconv_linattn_fwd(*a, o=torch.empty_like(want), stream=s)
     s.synchronize()
     assert torch.equal(bits(got), bits(want))
+
+
+def test_memory_of_a_call_on_another_stream_is_not_reused_under_it():
+    """What a call allocates belongs to the current stream, its work to another: the allocator must not hand the
+    workspace out again before that work is done. The other stream is held up by long products first; were the
+    workspace free, the fills below would take its place and write into it."""
+    q, k, v, ld, _ = make((1, 4096, 1, 128), (1, 4096, 1, 128), 17)
+    a = [x.to(DEV) for x in (q, k, v, ld)]
+    want, fin, _ = cc.cconv_linattn_fwd(*a, want_final_state=True)
+    need = cc.cconv_linattn_fwd_workspace_bytes(1, 4096, 1, 128, 128)
+    assert need > 0
+    m = torch.randn(4096, 4096, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            m = m @ m * 1e-3
+    got, gfin, _ = cc.cconv_linattn_fwd(*a, want_final_state=True, stream=s)
+    junk = [torch.full((need,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(bits(got), bits(want)) and torch.equal(bits(gfin), bits(fin)) and len(junk) == 4
 
 
 def test_binding_refusals():

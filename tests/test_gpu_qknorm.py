@@ -144,6 +144,25 @@ def test_bad_positions_write_nothing(T, bad):
         assert bool((o == 7.0).all())
 
 
+def test_rows_past_32_bit_offsets():
+    """2.2e9 elements a tensor: the last rows come out as they do alone, bit for bit."""
+    T, H = 270000, 64
+    x = torch.randn(1, 64, H, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    big = torch.zeros(1, T, H, 128, dtype=torch.bfloat16, device=DEV)
+    assert big.numel() > 2**31
+    big[:, -64:] = x
+    w, tab = torch.ones(128, device=DEV), table_of(T, 64).to(DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)[None]
+    k, kp = big[:, :, :1], x[:, :, :1]
+    yq, yk, st = cc.cconv_qknorm_fwd(big, k, w, w, tab, positions=pos)
+    zq, zk, _ = cc.cconv_qknorm_fwd(x, kp, w, w, tab, positions=pos[:, -64:].contiguous())
+    assert int(st) == 0 and torch.equal(bits(yq[:, -64:]), bits(zq)) and torch.equal(bits(yk[:, -64:]), bits(zk))
+    del yq
+    dq, dk, _, _, _ = cc.cconv_qknorm_bwd(big, k, big, k, w, w, tab, positions=pos)
+    eq, ek, _, _, _ = cc.cconv_qknorm_bwd(x, kp, x, kp, w, w, tab, positions=pos[:, -64:].contiguous())
+    assert torch.equal(bits(dq[:, -64:]), bits(eq)) and torch.equal(bits(dk[:, -64:]), bits(ek))
+
+
 def test_outputs_in_wider_rows_and_guards():
     x = torch.randn(2, 5, 3, 96, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(DEV)
     w, tab = torch.ones(96, device=DEV), table_of(8, 32).to(DEV)
