@@ -230,40 +230,17 @@ struct Wave {
     }
 
     // S = S * keep + k^T (weight * v), where row j of the chunk (n rows) has weight gamma * a^(n-shift-j) *
-    // more. The weighted v is taken as a sum of two bf16 values (the second holds what the first rounds
-    // off), so the state keeps about 17 bits of every term.
-    template <bool KEEP, int PRE>
+    // more. The weighted v enters the products as a sum of three bf16 values, which holds its 24 bits: the state is
+    // what fp32 sums make of exact terms, at 1e-7 to 5e-7 of its norm. LEAN, where registers do not reach for the
+    // third value, it enters as two, 17 bits: 2e-6 of the norm. (The third value costs the walk of
+    // [4, 8192, 32 heads, 128] 6%; in the joint walk of dk and dv it cost 60%, by spills.)
+    template <bool KEEP>
     __device__ __forceinline__ void update(const uint16_t* lk, const uint16_t* lv, int col0, const Table& tab, int n, bool special,
                                            float more) {
         const int lane = anew(threadIdx.x % kWave, LEAN), i16 = lane % 16, g = lane / 16;
-        // a half's first PRE loads are issued before its values are weighted, the second half's (registers
-        // allowing) before the first's products: their latency is behind other work
-        constexpr bool kBoth = PRE > 2;
-        u32x4 vf[2][NM], kf[2][PRE];
-        auto fetch = [&](int h) {
-#pragma unroll
-            for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
-#pragma unroll
-            for (int t = 0; t < PRE; ++t) kf[h][t] = columns<DK, false>(lk, t, h, i16, g);
-            loads_first();
-        };
-        fetch(0);
-        if constexpr (KEEP) {
-            const float an = n == kChunk ? aC : power(g2, n);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[t][m][r] *= an;
-        }
-        u32x4 hi[NM], lo[NM];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h == 1 && !kBoth) fetch(1);
-            f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 4 * g),
-                           *reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 16 + 4 * g)};
-            float w[8];
+        auto weights = [&](int h, float (&w)[8]) {
+            const f32x4 wt[2] = {*reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 4 * g),
+                                 *reinterpret_cast<const f32x4*>(tab.weight + 32 * h + 16 + 4 * g)};
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = KEEP ? wt[e / 4][e % 4] : wt[e / 4][e % 4] * more;
             if (n < kChunk) {  // rows past the end hold zeros; their weight only has to be finite
@@ -273,29 +250,94 @@ struct Wave {
                     w[e] = gamma * power(g2, left < 0 ? 0 : left) * more;
                 }
             }
-            auto split = [&](auto&& rest) {
+        };
+        // weighted rows as three bf16 values: the second holds what the first rounds off, the third what the second
+        auto split = [](u32x4 v, const float (&w)[8], u32x4& hi, u32x4& mid, u32x4& lo, auto&& rest) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float u0 = bf16_lo(v[d]) * w[2 * d], u1 = bf16_hi(v[d]) * w[2 * d + 1];
+                const uint32_t x = pack_bf16x2(u0, u1);
+                const float r0 = rest(u0 - bf16_lo(x)), r1 = rest(u1 - bf16_hi(x));
+                const uint32_t y = pack_bf16x2(r0, r1);
+                hi[d] = x;
+                mid[d] = y;
+                lo[d] = pack_bf16x2(r0 - bf16_lo(y), r1 - bf16_hi(y));
+            }
+        };
+        // of an infinite or NaN value the rest is made finite: the first part carries it
+        auto finite = [](float x) { return __builtin_amdgcn_fmed3f(x, -1e38f, 1e38f); };
+        auto shrink = [&] {
+            if constexpr (KEEP) {
+                const float an = n == kChunk ? aC : power(g2, n);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) S[t][m][r] *= an;
+            }
+        };
+        if constexpr (LEAN) {  // few registers: two values, and the keys loaded as they are used
+            u32x4 vf[NM], hi[NM], lo[NM];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) vf[m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
+                const u32x4 first = columns<DK, false>(lk, 0, h, i16, g);
+                loads_first();
+                if (h == 0) shrink();
+                float w[8];
+                weights(h, w);
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
-                        const float u0 = bf16_lo(vf[h][m][d]) * w[2 * d], u1 = bf16_hi(vf[h][m][d]) * w[2 * d + 1];
-                        const uint32_t x = pack_bf16x2(u0, u1);
-                        hi[m][d] = x;
-                        lo[m][d] = pack_bf16x2(rest(u0 - bf16_lo(x)), rest(u1 - bf16_hi(x)));
+                        const float u0 = bf16_lo(vf[m][d]) * w[2 * d], u1 = bf16_hi(vf[m][d]) * w[2 * d + 1];
+                        hi[m][d] = pack_bf16x2(u0, u1);
+                        lo[m][d] = pack_bf16x2(finite(u0 - bf16_lo(hi[m][d])), finite(u1 - bf16_hi(hi[m][d])));
                     }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const u32x4 k = t == 0 ? first : columns<DK, false>(lk, t, h, i16, g);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, lo[m], S[t][m]);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, hi[m], S[t][m]);
+                }
+            }
+        } else {  // a half's loads are issued before its values are weighted, the second half's before the first's
+                  // products: their latency is behind other work
+            u32x4 vf[2][NM], kf[2][NT], hi[NM], mid[NM], lo[NM];
+            auto fetch = [&](int h) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) vf[h][m] = columns<COLSV, false>(lv, col0 / 16 + m, h, i16, g);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) kf[h][t] = columns<DK, false>(lk, t, h, i16, g);
+                loads_first();
             };
-            if (!LEAN && __builtin_expect(!special, 1))
-                split([](float x) { return x; });
-            else  // of an infinite or NaN value the rest is made finite: the first part carries it
-                split([](float x) { return __builtin_amdgcn_fmed3f(x, -1e38f, 1e38f); });
-            if (h == 0 && kBoth) fetch(1);
+            fetch(0);
+            shrink();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const u32x4 k = t < PRE ? kf[h][t < PRE ? t : 0] : columns<DK, false>(lk, t, h, i16, g);
+            for (int h = 0; h < 2; ++h) {
+                float w[8];
+                weights(h, w);
+                if (__builtin_expect(!special, 1)) {
 #pragma unroll
-                for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, lo[m], S[t][m]);
+                    for (int m = 0; m < NM; ++m) split(vf[h][m], w, hi[m], mid[m], lo[m], [](float x) { return x; });
+                } else {
 #pragma unroll
-                for (int m = 0; m < NM; ++m) S[t][m] = mfma(k, hi[m], S[t][m]);
+                    for (int m = 0; m < NM; ++m) split(vf[h][m], w, hi[m], mid[m], lo[m], finite);
+                }
+                if (h == 0) fetch(1);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf[h][t], lo[m], S[t][m]);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf[h][t], mid[m], S[t][m]);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[t][m] = mfma(kf[h][t], hi[m], S[t][m]);
+                }
             }
         }
     }
@@ -610,7 +652,6 @@ __device__ __forceinline__ void enter(Wave<DK, NV, COLSV, LEAN>& w, const WalkAr
 template <int DK, int NV, int VEC, bool WIDE>
 __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV;
-    constexpr int PRE = DK == 256 ? 4 : DK / 16;  // as the registers allow
     __shared__ __align__(16) uint16_t lk[2][kChunk * DK];
     __shared__ __align__(16) uint16_t lv[2][kChunk * DVB];
     __shared__ __align__(16) uint16_t ls[2][DVB * DK];
@@ -680,7 +721,7 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            w.template update<true, PRE>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
+            w.template update<true>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
                                            __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0, 1.0f);
             if (left > kChunk) {
                 stage(c0 + kChunk);
@@ -785,7 +826,7 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
         lds_barrier();
         for (int c0 = 0; c0 < rows; c0 += kChunk) {
             const int b = (c0 / kChunk) & 1, left = rows - c0;
-            w.template update<true, 1>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
+            w.template update<true>(lk[b], lv[b], w4 * NV, tab, left < kChunk ? left : kChunk,
                                            __builtin_amdgcn_readfirstlane(odd_chunk[b]) == c0, 1.0f);
             if (left > kChunk) {
                 stage(c0 + kChunk);
@@ -832,7 +873,7 @@ __global__ __launch_bounds__(DK == 256 ? 256 : 512, DK == 256 ? 1 : 2) void ccon
         sk.load(kChunk);
         sv.load(kChunk);
     }
-    Wave<DK, NV, DVB> w;
+    Wave<DK, NV, DVB, DK == 256> w;
     w.open(a.log_decay[s.hv], a.gamma, a.shift);
     tab.fill(a.log_decay[s.hv], a.gamma, a.shift, threadIdx.x);
     if (threadIdx.x < 2 * GROUPS) (&odd_chunk[0][0])[threadIdx.x] = -1;
@@ -861,7 +902,7 @@ __global__ __launch_bounds__(DK == 256 ? 256 : 512, DK == 256 ? 1 : 2) void ccon
         if (c + GROUPS < chunks) stage(c + GROUPS, b ^ 1);
         if (c < chunks) {
             const uint16_t* lk = mine + b * kTile;
-            w.template update<false, DK == 256 ? 4 : DK / 16>(lk, lk + kChunk * DK, wave * NV, tab, kChunk, special, more);
+            w.template update<false>(lk, lk + kChunk * DK, wave * NV, tab, kChunk, special, more);
         }
         more *= skip;
         lds_barrier();
