@@ -17,7 +17,8 @@
 // k, v and the copy of the state are double-buffered, so a chunk costs one barrier, and its time is the
 // longer of the two waves' parts, not their sum. At 128 channels a side a workgroup alone on its CU takes
 // 2.9 us a chunk (5300 cycles of row waves, 5500 of state waves); with every wave doing both parts in turn and
-// three barriers a chunk it took 4.5 us, and the walk of [4, 8192, 32 heads, 128] 244 us instead of 204 us.
+// three barriers a chunk it took 4.5 us, and the walk of [4, 8192, 32 heads, 128] 244 us instead of 204 us (both
+// with weighted rows of two values, see Wave::update).
 // Every product is laid out so that what one leaves in registers is what the next takes: scores as
 // p^T[m = row j][n = row i] are the right operand of o^T = v^T p^T, with v read from LDS by the transposing
 // loads; rows of q go from memory straight to fragments.
@@ -646,9 +647,9 @@ __device__ __forceinline__ void enter(Wave<DK, NV, COLSV, LEAN>& w, const WalkAr
 }
 
 // The walk: four row waves, then four state waves, of NV value channels each, which also stage the chunks
-// (staged by all eight, the row waves' part was the longer: 242 us instead of 216 us). 204 us at
-// [4, 8192, 32 heads, 128] for the 1.08 GB of q, k, v and o, 5.3 TB/s: near what memory gives, with the
-// matrix units at 32% and the vector units at 54%.
+// (staged by all eight, the row waves' part was the longer: 242 us instead of 216 us). 217 us at
+// [4, 8192, 32 heads, 128] for the 1.08 GB of q, k, v and o, 5.0 TB/s: near what memory gives, with the
+// matrix units at 39% and the vector units at 42% of the time.
 template <int DK, int NV, int VEC, bool WIDE>
 __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) {
     constexpr int DVB = 4 * NV;
@@ -737,8 +738,8 @@ __global__ __launch_bounds__(512, 2) void cconv_linattn_walk_kernel(WalkArgs a) 
 
 // Two walks over the same rows whose states are each other's transposes: dv (rows k, keys q, values do)
 // and dk (rows v, keys do, values q). One set of state waves serves both, the second set of row waves
-// reading the state's copy by columns; q and do are staged once. 340 us at [4, 8192, 32 heads, 128] for the
-// 1.61 GB of q, k, v, do, dk and dv, 4.7 TB/s; as two walks they took 2 x 244 us and a second pass for the
+// reading the state's copy by columns; q and do are staged once. 330 us at [4, 8192, 32 heads, 128] for the
+// 1.61 GB of q, k, v, do, dk and dv, 4.9 TB/s; as two walks they took 2 x 244 us and a second pass for the
 // segments' sums. Three waves on every SIMD leave each 168 registers: a few row addresses spill.
 template <int DK, int DV, int VEC, bool WIDE>
 __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a, SecondWalk z) {
@@ -844,7 +845,7 @@ __global__ __launch_bounds__(768, 3) void cconv_linattn_walk2_kernel(WalkArgs a,
 // segment's last to its first: their weights then only grow smaller, so the state needs no scaling, and
 // the rows read last are those that the walk after it reads first. A segment is summed in `sub` parts, each
 // by a workgroup of its own, in which GROUPS sets of four waves take every GROUPS-th chunk: a set alone on its
-// CU has nothing to do while it waits for its own loads. 68 us for the 268 MB of k and v of the first halves of
+// CU has nothing to do while it waits for its own loads. 69 us for the 268 MB of k and v of the first halves of
 // [4, 8192, 32 heads, 128], 3.9 TB/s, bound by the latency of a set's chunk.
 template <int DK, int NV, int VEC>
 __global__ __launch_bounds__(DK == 256 ? 256 : 512, DK == 256 ? 1 : 2) void cconv_linattn_states_kernel(WalkArgs a) {
