@@ -101,6 +101,9 @@ SHAPES = [
     (2, 64, 1, 1, 128, 128), (1, 65, 3, 3, 96, 80), (1, 127, 1, 2, 100, 60), (1, 128, 2, 2, 33, 47), (1, 129, 1, 3, 72, 136),
     (1, 200, 1, 1, 256, 256), (2, 300, 1, 2, 128, 256), (1, 700, 1, 1, 128, 128), (1, 577, 2, 2, 256, 64), (1, 5, 1, 1, 1, 1),
     (1, 70, 1, 1, 8, 200), (1, 1100, 1, 2, 64, 64),
+    # several segments of every width and kind of load
+    (1, 650, 1, 1, 64, 128), (1, 651, 1, 2, 128, 64), (1, 520, 2, 2, 100, 60), (1, 521, 1, 1, 33, 47), (2, 523, 1, 3, 72, 136),
+    (1, 449, 1, 1, 256, 256), (1, 450, 1, 1, 40, 256),
 ]
 
 
