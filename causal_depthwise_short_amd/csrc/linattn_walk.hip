@@ -505,7 +505,7 @@ __device__ __forceinline__ void row_outputs(const uint16_t* lk, const uint16_t* 
         p[jb] = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
     stores();
-    // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (a relative 2^-9 of each
+    // o^T = S^T q^T. The state's copy is rounded to bf16 as a matrix operand (at most 2^-8 of each
     // entry, as the products' other operand has; the state itself stays in 32 bits).
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
